@@ -376,6 +376,75 @@ fm_status fm_golden_labels(const float *scores, int64_t ld, int T, int n_layers,
                            int32_t *label_ptr, int32_t *label_idx, float *label_score,
                            int64_t cap, void *ws, size_t ws_bytes, void *stream);
 
+/*
+ * ---- attention over a paged key/value cache ---------------------------------------------------
+ *
+ * A key/value cache is an fm_kv_desc whose pools come in pairs: pool[2 l] holds the keys and
+ * pool[2 l + 1] the values of layer l.  Each is an array [n_phys_pages][n_kv_heads][64][row]; row
+ * is head_dim values of float32 or bf16, or (FM_FP8_E4M3_SCALED132, head_dim 128) 128 E4M3FN codes
+ * and their float32 scale.  With one kv head that is the compressed-key pool's layout.  head_dim
+ * is 64 or 128 here.  Block table, lengths and page bounds are as above, except that entries of
+ * an unmapped page (block-table value outside [0, n_phys_pages), e.g. -1 for a page a window has
+ * left behind) are simply not visible.  A page is read whole: all 64 entries of a mapped page
+ * must be readable memory, what the entries past seq_lens[b] hold does not matter.
+ *
+ * Query rows of one layer.  The rows of request b are q_start[b] .. q_start[b + 1] - 1, and they
+ * are the request's last entries: row i of n sits at position seq_lens[b] - n + i, its own key
+ * already in the cache.  Rows before q_start[0] or from q_start[B] on are neither read nor
+ * written.  Query head h reads kv head h / (n_heads / n_kv_heads).  q and out hold [n_heads,
+ * head_dim] a row, rows q_ld / out_ld elements apart (>= n_heads * head_dim, a multiple of 16
+ * bytes); out has q's type and must not overlap q.  (q_dtype, key_dtype): (F32, F32), (BF16, BF16),
+ * (BF16, SCALED132).  Device preconditions: q_start ascending and <= T, at most max_rows rows a
+ * request, seq_lens[b] <= max_seq_len; rows past max_rows are left as they were, longer lengths
+ * are cut.
+ */
+typedef struct {
+    const void *q;
+    fm_dtype q_dtype;           /* FM_F32 or FM_BF16 */
+    int64_t q_ld;
+    void *out;
+    int64_t out_ld;
+    float *lse;                 /* [T, n_heads] or NULL: ln sum_s exp(scale q . k_s) */
+    const int32_t *q_start;     /* [B + 1] */
+    int T;                      /* rows of q, out and lse */
+    int max_rows;               /* host-side upper bound of a request's rows */
+    int n_heads, n_kv_heads;    /* n_heads a multiple of n_kv_heads */
+    float scale;                /* > 0 (usually head_dim^-0.5) */
+    int layer;                  /* pools 2 layer and 2 layer + 1 */
+} fm_attn_desc;
+
+/* Workspace bytes of the two calls below (0: none needed). */
+size_t fm_attend_workspace_bytes(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window,
+                                 int64_t n_sink);
+
+/*
+ * Causal attention with a sliding window and first entries that stay visible.  A row at position
+ * p sees the entries s <= p with s > p - window or s < n_sink (CSA page, section 4: window
+ * attention beside the compressed entries; the same n_sink / recent vocabulary as
+ * fm_resident_mask).  out = sum_s softmax(scale q . k_s) v_s; a row that sees nothing gets zeros
+ * and lse -inf.  window >= 1 (itself included; max_seq_len or more: plain causal), n_sink >= 0.
+ * Accuracy: products accumulate in float32, statistics and sums are float32; over bf16 and fp8
+ * caches the probabilities are rounded to bf16 for the product with the values (2^-9 relative
+ * each), and the output once.  Masked entries may hold anything, NaN and infinities included; a
+ * visible NaN or infinity has the effect IEEE arithmetic gives it, except that a row whose every
+ * score is -inf counts as one that sees nothing.  Deterministic.
+ * ws 256-byte aligned, ws_bytes >= fm_attend_workspace_bytes, contents irrelevant.  T = 0 is a no-op.
+ */
+fm_status fm_attend_window(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window,
+                           int64_t n_sink, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The same for a tree of drafted tokens.  The n rows of a request are its drafts, entries
+ * seq_len - n .. seq_len - 1 of the cache; the entries before them are committed.  Bit j of word
+ * j / 64 of tree_mask[t * mask_ld ..] says that row t sees draft j of its request (itself and its
+ * ancestors; bits from n on are ignored).  Committed entries are visible by window and n_sink
+ * with the row at position seq_len - n + (its mask's set bits) - 1, i.e. at its depth; drafts by
+ * the mask alone.  max_rows <= 64 mask_ld.
+ */
+fm_status fm_attend_tree(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t *tree_mask,
+                         int64_t mask_ld, int64_t window, int64_t n_sink, void *ws,
+                         size_t ws_bytes, void *stream);
+
 /* Static description of a status code. */
 const char *fm_status_string(fm_status s);
 

@@ -30,7 +30,8 @@ Q_DTYPES = {"f32": FM_F32, "bf16": FM_BF16, "fp8": FM_FP8_E4M3}
 EXPORTS = ["fm_index_logits", "fm_index_topk", "fm_resident_mask", "fm_topk512", "fm_score_resident",
            "fm_score_resident_noalloc", "fm_score_resident_cells", "fm_densest_pages", "fm_workspace_bytes",
            "fm_encode_queries", "fm_encode_workspace_bytes", "fm_golden_labels",
-           "fm_golden_workspace_bytes", "fm_status_string", "fm_last_error", "fm_version"]
+           "fm_golden_workspace_bytes", "fm_attend_workspace_bytes", "fm_attend_window", "fm_attend_tree",
+           "fm_status_string", "fm_last_error", "fm_version"]
 
 
 class FmError(RuntimeError):
@@ -61,6 +62,13 @@ class EncoderDesc(C.Structure):
                 ("rope_orig_len", C.c_int), ("beta_fast", C.c_float), ("beta_slow", C.c_float)]
 
 
+class AttnDesc(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_dtype", C.c_int), ("q_ld", C.c_int64), ("out", C.c_void_p),
+                ("out_ld", C.c_int64), ("lse", C.c_void_p), ("q_start", C.c_void_p), ("T", C.c_int),
+                ("max_rows", C.c_int), ("n_heads", C.c_int), ("n_kv_heads", C.c_int),
+                ("scale", C.c_float), ("layer", C.c_int)]
+
+
 _lib = None
 
 
@@ -89,9 +97,13 @@ def lib():
                                        P, P, P, I64, P, C.c_size_t, P]
         L.fm_golden_workspace_bytes.argtypes = [C.c_int, C.c_int, I64, C.c_int]
         L.fm_golden_workspace_bytes.restype = C.c_size_t
+        L.fm_attend_workspace_bytes.argtypes = [P, P, I64, I64]
+        L.fm_attend_workspace_bytes.restype = C.c_size_t
+        L.fm_attend_window.argtypes = [P, P, I64, I64, P, C.c_size_t, P]
+        L.fm_attend_tree.argtypes = [P, P, P, I64, I64, I64, P, C.c_size_t, P]
         for f in ("fm_index_logits", "fm_index_topk", "fm_resident_mask", "fm_topk512", "fm_score_resident",
                   "fm_score_resident_noalloc", "fm_score_resident_cells", "fm_densest_pages", "fm_encode_queries",
-                  "fm_golden_labels"):
+                  "fm_golden_labels", "fm_attend_window", "fm_attend_tree"):
             getattr(L, f).restype = C.c_int
         L.fm_workspace_bytes.argtypes = [C.c_int, C.c_int, I64]
         L.fm_workspace_bytes.restype = C.c_size_t
@@ -130,14 +142,14 @@ def _check(status: int) -> None:
 
 # ----------------------------------------------------------------------------- descriptors
 def kv_desc(pools, key_dtype: str, block_table, seq_lens, max_seq_len: int,
-            n_phys_pages: int | None = None) -> KvDesc:
+            n_phys_pages: int | None = None, head_dim: int = 128) -> KvDesc:
     d = KvDesc()
     for i, p in enumerate(pools):
         d.pool[i] = _ptr(p)
     d.n_pools = len(pools)
     d.key_dtype = KEY_DTYPES[key_dtype]
     d.page_size = PAGE
-    d.head_dim = 128
+    d.head_dim = int(head_dim)
     d.block_table = _ptr(block_table)
     d.bt_ld = block_table.shape[1]
     d.seq_lens = _ptr(seq_lens)
@@ -246,6 +258,36 @@ def fm_encode_queries(desc: EncoderDesc, hidden, T: int, pos, q, w, ws, ws_bytes
                       stream=None) -> None:
     _check(lib().fm_encode_queries(C.byref(desc), _ptr(hidden), int(T), _ptr(pos), _ptr(q),
                                    _ptr(w), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def attn_desc(q, q_dtype: str, out, q_start, max_rows: int, *, n_kv_heads: int, scale: float, lse=None,
+              layer: int = 0) -> AttnDesc:
+    """fm_attn_desc over q and out [T, n_heads, head_dim] (rows may be strided, heads packed)."""
+    for t in (q, out):
+        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            raise ValueError("q and out are [T, n_heads, head_dim] with packed heads")
+    if q.shape != out.shape:
+        raise ValueError("q and out differ in shape")
+    T, H, D = q.shape
+    return AttnDesc(_ptr(q), Q_DTYPES[q_dtype], q.stride(0) if T > 1 else H * D, _ptr(out),
+                    out.stride(0) if T > 1 else H * D, _ptr(lse), _ptr(q_start), T, int(max_rows), H,
+                    int(n_kv_heads), float(scale), int(layer))
+
+
+def fm_attend_workspace_bytes(a: AttnDesc, kv: KvDesc, window: int, n_sink: int) -> int:
+    return int(lib().fm_attend_workspace_bytes(C.byref(a), C.byref(kv), int(window), int(n_sink)))
+
+
+def fm_attend_window(a: AttnDesc, kv: KvDesc, window: int, n_sink: int, ws=None, ws_bytes: int = 0,
+                     stream=None) -> None:
+    _check(lib().fm_attend_window(C.byref(a), C.byref(kv), int(window), int(n_sink), _ptr(ws), int(ws_bytes),
+                                  _stream(stream)))
+
+
+def fm_attend_tree(a: AttnDesc, kv: KvDesc, tree_mask, mask_ld: int, window: int, n_sink: int, ws=None,
+                   ws_bytes: int = 0, stream=None) -> None:
+    _check(lib().fm_attend_tree(C.byref(a), C.byref(kv), _ptr(tree_mask), int(mask_ld), int(window), int(n_sink),
+                                _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
 def fm_golden_workspace_bytes(T: int, n_layers: int, ld: int, tau: int) -> int:

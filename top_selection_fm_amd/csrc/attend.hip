@@ -1,0 +1,906 @@
+// attend.hip -- attention of query rows over a paged key/value cache: causal with a sliding
+// window and first entries that stay visible (sinks), and the same for a tree of drafted tokens.
+//
+// Row r of a request and query head h (kv head h / G, G = n_heads / n_kv_heads):
+//   x_s = scale q . k_s over the visible entries s,  o = sum_s softmax(x)_s v_s,  lse = ln sum e^x_s.
+// The G heads of a kv head and a request's rows are flattened (row-major, heads inner) into the
+// columns of one problem, so the entries are read once for 32 or more of them.
+//
+// A wave holds 32 columns.  Scores are formed transposed, S^T = K Q^T (entries x columns), on
+// 32 x 32 MFMA tiles: lane j + 32 h then holds, for column j, the entries 8 (v / 4) + 4 h + v % 4
+// of accumulator register v, so the softmax statistics of a column are per-lane values (the two
+// halves of a column meet through one lane swap), and the exponentials are already where the
+// second product O^T = V^T P^T wants its B operand, if the entries of a k step are taken in that
+// order.  V^T's A operand comes from LDS through the transposing reads (ds_read_b64_tr_b16): no
+// shuffle and no LDS round trip for P.  Statistics, sums and outputs are float32; for bf16 and
+// fp8 caches the probabilities are rounded to bf16 for the second product (relative 2^-9 each,
+// like the rounding of the output itself), their sum is taken before the rounding.
+//
+// Two kernels share that inner step:
+//   attend_split_kernel  few columns (<= 64): the four waves of a workgroup hold the same columns
+//                        and each streams tiles of its own, without barriers; bound by memory.
+//   attend_tile_kernel   many columns: a wave has 32 of its own, and the workgroup's four waves
+//                        share each key/value tile; bound by MFMA and the exponentials.
+// Both can split the entries over several workgroups; attend_merge_kernel joins the parts.
+//
+// Masks: each lane forms a word of visible entries for a tile; tiles every column sees whole skip
+// the test.  A masked entry's key can hold anything (its score is replaced), and so can its
+// value: 0 * inf would reach the sum through the product, so tiles with masked entries are
+// searched for values that are not finite, and what those do is kept apart (Special, below).
+#include <type_traits>
+
+#include "fm_internal.h"
+
+namespace fm {
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+// A column's running maximum is raised only when a tile exceeds it by this many powers of two:
+// until then the exponentials stay below 2^8, far from overflow, and the sums need no rescaling.
+constexpr float kLazy = 8.f;
+
+__device__ __forceinline__ float other_half(float x) {     // the value of lane ^ 32
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(__lane_id() < 32 ? s[1] : s[0]);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const f32x2 v = {a, b};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ f32x16 mma_bf16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+template <int N> __device__ __forceinline__ void wait_vm() {     // s_waitcnt vmcnt(N), others left alone
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+}
+
+// A tile in LDS: E entries (rows) of D values, bf16 (64 rows) or float32 (32 rows), in 16-byte
+// pieces.  Row r's piece p sits at piece p ^ swz(r) of the row, so that the reads below touch
+// every bank group evenly: 16 rows at one piece (scores, bf16 and float32), or 8 rows at two
+// (transposing reads of bf16 values) or at eight (float32 values) neighbouring pieces.
+template <int FMT, int D>
+struct Tile {
+    static constexpr bool F32 = FMT == KEY_F32;
+    static constexpr int E = F32 ? 32 : 64;              // entries
+    static constexpr int SUB = E / 32;                   // 32-entry MFMA tiles
+    static constexpr int ROW = D * (F32 ? 4 : 2);        // bytes of a row
+    static constexpr int NP = ROW / 16;                  // pieces of a row
+    static constexpr int BYTES = E * ROW;
+    static constexpr int DT = D / 32;                    // 32-value tiles of the output
+    static constexpr int QR = F32 ? D / 8 : D / 16;      // 16-byte query registers of a lane
+
+    __device__ static __forceinline__ int swz_k(int r) {
+        if constexpr (F32) return (r & 3) | ((r & 4) << 1) | ((r & 8) >> 1);
+        else if constexpr (NP == 16) return r & 15;
+        else return (r >> 1) & 7;
+    }
+    __device__ static __forceinline__ int swz_v(int r) {
+        if constexpr (F32) return swz_k(r);
+        else if constexpr (NP == 16) return 2 * (r & 7);
+        else return 2 * ((r >> 1) & 3);
+    }
+};
+
+template <int FMT, int D> using QRegs = u32x4[Tile<FMT, D>::QR];
+template <int FMT, int D> using PRegs = u32x4[Tile<FMT, D>::SUB][2];
+template <int FMT, int D> using SRegs = f32x16[Tile<FMT, D>::SUB];
+
+// One problem's columns: position, limits and masks of the lane's row.
+struct Col {
+    int pos;              // position of the row
+    int lo, hi;           // entries [lo, hi) of the window, [0, sink) of the first ones
+    int sink;
+    bool valid;
+    const uint64_t *mask; // tree: the row's bits (bit j: entry base + j), or null
+    int base, n;
+};
+
+__device__ __forceinline__ uint64_t low_bits(int n) {     // bits 0 .. n - 1
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+__device__ __forceinline__ uint64_t range_bits(int a, int b, int s0) {   // entries [a, b) of s0 ..
+    return low_bits(b - s0) & ~low_bits(a - s0);
+}
+
+// The visible entries among s0 .. s0 + 63 of a column.
+__device__ __forceinline__ uint64_t visible(const Col &c, int s0, int64_t mask_ld) {
+    uint64_t w = range_bits(c.lo, c.hi, s0) | range_bits(0, c.sink, s0);
+    if (c.mask && s0 + 63 >= c.base && s0 < c.base + c.n) {
+        const int off = s0 - c.base;                      // bit of the tile's first entry
+        uint64_t d;
+        if (off < 0) {
+            d = c.mask[0] << -off;                        // -off <= 63
+        } else {
+            const int i = off >> 6, sh = off & 63;        // off < n <= 64 mask_ld
+            d = c.mask[i] >> sh;
+            if (sh && i + 1 < mask_ld) d |= c.mask[i + 1] << (64 - sh);
+        }
+        w |= d & range_bits(c.base, c.base + c.n, s0);
+    }
+    return w;
+}
+
+// The lane's column R of request b (rows row0 .. row0 + n - 1, len entries).
+__device__ __forceinline__ Col make_col(const AttendArgs &A, int R, int row0, int n, int len) {
+    Col c;
+    const int i = R / A.G;
+    c.valid = i < n;
+    c.n = n;
+    c.base = len - n;
+    c.pos = len - n + i;
+    c.mask = nullptr;
+    c.hi = c.pos + 1;
+    if (A.tree_mask) {
+        c.mask = A.tree_mask + (int64_t)(row0 + (c.valid ? i : 0)) * A.mask_ld;
+        int seen = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; j += 64) seen += __popcll(c.mask[j >> 6] & low_bits(n - j));
+        c.pos = c.base + seen - 1;
+        c.hi = c.base;
+    }
+    c.hi = max(c.hi, 0);
+    c.lo = max(c.pos - (A.window - 1), 0);
+    c.sink = min(A.n_sink, c.hi);
+    if (c.lo >= c.hi) c.lo = c.hi;
+    return c;
+}
+
+// Tiles of a workgroup's rows i0 .. i1: the first ones up to the sinks, then from the window on.
+struct Span {
+    int first;        // tiles 0 .. first - 1
+    int from, count;  // then tiles from ..; count in all
+    __device__ int at(int i) const { return i < first ? i : from + i - first; }
+};
+template <int E>
+__device__ __forceinline__ Span make_span(const AttendArgs &A, int i0, int i1, int n, int len) {
+    Span s{0, 0, 0};
+    const int hi = A.tree_mask ? len : len - n + i1 + 1;
+    if (i0 > i1 || hi <= 0) return s;
+    // a row of a tree sits at base - 1 or later
+    const int p0 = A.tree_mask ? len - n - 1 : len - n + i0;
+    const int lo = max(p0 - (A.window - 1), 0);
+    s.first = (min(A.n_sink, hi) + E - 1) / E;
+    s.from = max(lo / E, s.first);
+    s.count = s.first + max((hi + E - 1) / E - s.from, 0);
+    return s;
+}
+
+template <int FMT, int D>
+struct State {
+    f32x16 o[Tile<FMT, D>::DT];
+    float m, l;       // m: maximum in score units (both halves alike), l: the lane's own entries
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int t = 0; t < Tile<FMT, D>::DT; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[t][v] = 0.f;
+        m = kNegInf;
+        l = 0.f;
+    }
+};
+
+// The lane's queries: 16-byte pieces; rows past the problem read as zeros.
+template <int FMT, int D>
+__device__ __forceinline__ void load_q(QRegs<FMT, D> &q, const AttendArgs &A, int R, int row0,
+                                       int hk, bool valid) {
+    const int h = __lane_id() >> 5;
+    const int64_t row = row0 + R / A.G;
+    const int64_t at = row * A.q_ld + (int64_t)(hk * A.G + R % A.G) * D;
+    const uint8_t *p = (const uint8_t *)A.q + at * (FMT == KEY_F32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < Tile<FMT, D>::QR; ++i) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        q[i] = valid ? *(const u32x4 *)(p + 32 * i + 16 * h) : zero;
+    }
+}
+
+// S^T of one 32-entry tile.
+template <int FMT, int D>
+__device__ __forceinline__ f32x16 scores(const uint8_t *kt, int sub, const QRegs<FMT, D> &q) {
+    using TL = Tile<FMT, D>;
+    const int ln = __lane_id(), h = ln >> 5, r = ln & 31;
+    const uint8_t *row = kt + r * TL::ROW + 32 * sub * TL::ROW;
+    const int sw = TL::swz_k(r);                          // the same 32 rows further on
+    f32x16 s;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) s[v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < TL::QR; ++i) {
+        const u32x4 a = *(const u32x4 *)(row + 16 * ((2 * i + h) ^ sw));
+        if constexpr (TL::F32) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[c]), __uint_as_float(q[i][c]), s, 0, 0, 0);
+        } else {
+            s = mma_bf16(a, q[i], s);
+        }
+    }
+    return s;
+}
+
+// Column sums over the tile's entries: acc[d, column] += sum_e f(V[e, d]) P[e, column] for the 32
+// values of tile t, f applied to the operand registers.  bf16: P packed, f on pairs; float32: P
+// and f on single values.
+template <int FMT, int D, class F>
+__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, int t, const SRegs<FMT, D> &p,
+                                        const PRegs<FMT, D> &pk, f32x16 acc, F f) {
+    using TL = Tile<FMT, D>;
+    const int ln = __lane_id(), h = ln >> 5;
+    if constexpr (TL::F32) {
+        const int j = ln & 31;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int r = 8 * (v >> 2) + 4 * h + (v & 3);
+            const uint32_t x = *(const uint32_t *)(vt + r * TL::ROW + 16 * ((8 * t + (j >> 2)) ^ TL::swz_v(r)) + 4 * (j & 3));
+            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f(x)), p[0][v], acc, 0, 0, 0);
+        }
+    } else {
+        const int i = ln & 15, g = (ln >> 4) & 1;
+        const int piece = 4 * t + 2 * g + ((i & 3) >> 1), r = 4 * h + (i >> 2);
+        // rows r, r + 8, ..: one swizzle for all
+        const uint8_t *lane = vt + r * TL::ROW + 16 * (piece ^ TL::swz_v(r)) + 8 * (i & 1);
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const uint8_t *at = lane + (32 * sub + 16 * ks) * TL::ROW;
+                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+                const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4 *)(at + 8 * TL::ROW)));
+                const u32x4 x = {f(a[0]), f(a[1]), f(b[0]), f(b[1])};
+                acc = mma_bf16(x, pk[sub][ks], acc);
+            }
+    }
+    return acc;
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void pack_p(const SRegs<FMT, D> &p, PRegs<FMT, D> &pk) {
+    if constexpr (FMT != KEY_F32) {
+#pragma unroll
+        for (int sub = 0; sub < Tile<FMT, D>::SUB; ++sub)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    pk[sub][ks][w] = pack_bf16(p[sub][8 * ks + 2 * w], p[sub][8 * ks + 2 * w + 1]);
+    }
+}
+
+// Columns' sums that a visible value which is not finite has reached: bits (column, value) of
+// 0 * inf or NaN, +inf and -inf, applied to the sums before they leave the wave.
+template <int D>
+struct Special {
+    uint32_t any;
+    uint32_t nan[32][D / 32], up[32][D / 32], down[32][D / 32];
+    uint32_t vis[32][2], dead[32][2];     // scratch: the columns' visible entries, and those with p = 0
+};
+template <int D>
+__device__ __forceinline__ void clear_special(Special<D> &sp) {
+    uint32_t *x = &sp.any;
+#pragma unroll 1
+    for (int i = __lane_id(); i < (int)(sizeof(Special<D>) / 4); i += 64) x[i] = 0;
+}
+
+// Marks what the tile's infinities and NaNs do to the columns that see them.  Rolled loops over
+// the tile in LDS: such tiles are rare, and the wave's registers stay where they are.
+template <int FMT, int D>
+__device__ __forceinline__ void mark_special(const uint8_t *vt, const SRegs<FMT, D> &p, uint64_t vis,
+                                             Special<D> &sp) {
+    using TL = Tile<FMT, D>;
+    const int ln = __lane_id(), h = ln >> 5;
+    uint32_t dead[2] = {0u, 0u};
+#pragma unroll
+    for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            dead[sub] |= p[sub][v] == 0.f ? 1u << (8 * (v >> 2) + (v & 3)) : 0u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t own = dead[i] << (4 * h);
+        const uint32_t both = own | __float_as_uint(other_half(__uint_as_float(own)));
+        if (ln < 32) {
+            sp.vis[ln][i] = (uint32_t)(vis >> (32 * i));
+            sp.dead[ln][i] = both;
+        }
+    }
+    if (ln == 0) sp.any = 1;
+    __builtin_amdgcn_wave_barrier();
+    constexpr int W = TL::F32 ? 1 : 2;                     // values of a dword
+#pragma unroll 1
+    for (int x = ln; x < TL::BYTES / 4; x += 64) {
+        const int r = x / (TL::ROW / 4), at = x % (TL::ROW / 4);
+        const int d0 = (4 * ((at >> 2) ^ TL::swz_v(r)) + (at & 3)) * W;
+        const uint32_t word = *(const uint32_t *)(vt + 4 * x);
+#pragma unroll 1
+        for (int k = 0; k < W; ++k) {
+            const uint32_t y = W == 1 ? word : k ? word & 0xffff0000u : word << 16;
+            if ((y & 0x7f800000u) != 0x7f800000u) continue;
+            const int d = d0 + k;
+            const bool isnan = (y & 0x007fffffu) != 0;
+#pragma unroll 1
+            for (int c = 0; c < 32; ++c) {
+                if (!((sp.vis[c][r >> 5] >> (r & 31)) & 1)) continue;
+                const bool zero = (sp.dead[c][r >> 5] >> (r & 31)) & 1;
+                uint32_t *to = isnan || zero ? sp.nan[c] : y >> 31 ? sp.down[c] : sp.up[c];
+                atomicOr(&to[d >> 5], 1u << (d & 31));
+            }
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void apply_special(const Special<D> &sp, State<FMT, D> &st) {
+    if (!sp.any) return;
+    const int ln = __lane_id(), j = ln & 31, h = ln >> 5;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int bit = 8 * (v >> 2) + 4 * h + (v & 3);
+            if ((sp.up[j][t] >> bit) & 1) st.o[t][v] += __builtin_inff();
+            if ((sp.down[j][t] >> bit) & 1) st.o[t][v] -= __builtin_inff();
+            if ((sp.nan[j][t] >> bit) & 1) st.o[t][v] = __builtin_nanf("");
+        }
+}
+
+// A dword of values with those that are not finite taken as zeros.
+template <bool F32>
+__device__ __forceinline__ uint32_t finite_only(uint32_t x) {
+    if constexpr (F32) return (x & 0x7f800000u) == 0x7f800000u ? 0u : x;
+    const uint32_t lo = (x & 0x00007f80u) == 0x00007f80u ? 0u : 0x0000ffffu;
+    const uint32_t hi = (x & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u;
+    return x & (lo | hi);
+}
+
+// Whether any value of the tile is not finite (a wave-uniform answer).
+template <int FMT, int D>
+__device__ __forceinline__ bool any_special(const uint8_t *vt) {
+    using TL = Tile<FMT, D>;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < TL::BYTES / 1024; ++i) {
+        const u32x4 x = *(const u32x4 *)(vt + 1024 * i + 16 * __lane_id());
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            if constexpr (TL::F32) bad |= (x[w] & 0x7f800000u) + 0x00800000u;
+            else bad |= ((x[w] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        }
+    }
+    return __ballot((bad & 0x80008000u) != 0) != 0;
+}
+
+// The softmax step of a tile for one column: the scores become exponentials, the state is rescaled.
+// c: scale * log2 e.  ks, vs: the entries' fp8 scales of the tile (null otherwise).
+template <int FMT, int D>
+__device__ __forceinline__ void soften(SRegs<FMT, D> &s, bool masked,
+                                       uint64_t vis, float c, const float *ks, const float *vs, State<FMT, D> &st) {
+    using TL = Tile<FMT, D>;
+    const int h = __lane_id() >> 5;
+    if constexpr (FMT == KEY_FP8) {
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const f32x4 k = *(const f32x4 *)(ks + 32 * sub + 8 * a + 4 * h);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) s[sub][4 * a + b] *= k[b];
+            }
+    }
+    if (masked) {
+        const uint64_t w = vis >> (4 * h);
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                s[sub][v] = (w >> (32 * sub + 8 * (v >> 2) + (v & 3))) & 1 ? s[sub][v] : kNegInf;
+    }
+    float mx = s[0][0];
+#pragma unroll
+    for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[sub][v]);
+    mx = fmaxf(mx, other_half(mx));
+    if (__ballot((mx - st.m) * c > kLazy || (st.m == kNegInf && mx > kNegInf))) {
+        const float m = fmaxf(st.m, mx);
+        const float a = st.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((st.m - m) * c);
+        st.m = m;
+        st.l *= a;
+#pragma unroll
+        for (int t = 0; t < TL::DT; ++t)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) st.o[t][v] *= a;
+    }
+    const float mc = st.m == kNegInf ? 0.f : st.m * c;
+    float sum = 0.f;
+#pragma unroll
+    for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            s[sub][v] = __builtin_amdgcn_exp2f(fmaf(s[sub][v], c, -mc));
+            sum += s[sub][v];
+        }
+    st.l += sum;
+    if constexpr (FMT == KEY_FP8) {
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                const f32x4 k = *(const f32x4 *)(vs + 32 * sub + 8 * a + 4 * h);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int v = 4 * a + b;
+                    const float y = s[sub][v] * k[b];
+                    // a masked entry's scale may be anything
+                    s[sub][v] = masked && !((vis >> (32 * sub + 8 * a + 4 * h + b)) & 1) ? 0.f : y;
+                }
+            }
+    }
+}
+
+template <int FMT, int D>
+__device__ __forceinline__ void add_values(const uint8_t *vt, const SRegs<FMT, D> &p, bool masked,
+                                           uint64_t vis, State<FMT, D> &st, Special<D> &sp) {
+    PRegs<FMT, D> pk;
+    pack_p<FMT, D>(p, pk);
+    if (masked && any_special<FMT, D>(vt)) {
+        mark_special<FMT, D>(vt, p, vis, sp);
+#pragma unroll
+        for (int t = 0; t < Tile<FMT, D>::DT; ++t)
+            st.o[t] = weigh<FMT, D>(vt, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < Tile<FMT, D>::DT; ++t)
+        st.o[t] = weigh<FMT, D>(vt, t, p, pk, st.o[t], [](uint32_t x) { return x; });
+}
+
+// Copy of a tile from the pool straight into LDS: instruction n of the tile moves 64 pieces.  The
+// lane's source offset within an instruction's 1 KB is one value but for an exclusive or with n's
+// part of the swizzle.
+template <int FMT, int D, bool KEYS>
+__device__ __forceinline__ void copy_pieces(const uint8_t *src, uint8_t *dst, int n) {
+    using TL = Tile<FMT, D>;
+    constexpr int RI = 1024 / TL::ROW;                    // rows of an instruction
+    const int ln = __lane_id(), r = ln / TL::NP, at = ln % TL::NP;
+    auto swz = [](int r) { return KEYS ? TL::swz_k(r) : TL::swz_v(r); };
+    const uint32_t lane = (uint32_t)(r * TL::ROW + 16 * (at ^ swz(r)));
+    const uint32_t ofs = lane ^ (uint32_t)(16 * swz(RI * n));   // swz(RI n + r) = swz(RI n) ^ swz(r)
+    __builtin_amdgcn_global_load_lds((const void *)(src + 1024 * n + ofs), (lds_void *)(dst + 1024 * n), 16, 0, 0);
+}
+
+// fp8 tiles pass through registers: 16 codes a piece, widened exactly to bf16.
+template <int N>
+struct CodeRegs {
+    u32x4 x[N];
+    float scale;
+};
+template <int N, int NT>   // N pieces a thread, NT threads
+__device__ __forceinline__ void load_codes(CodeRegs<N> &c, const uint8_t *src, int tid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int piece = tid + NT * i;
+        c.x[i] = *(const u32x4_u *)(src + (piece >> 3) * kRowFp8 + 16 * (piece & 7));
+    }
+    if (tid < 64) c.scale = *(const float *)(src + tid * kRowFp8 + kDim);
+}
+template <int N, int NT, bool KEYS>
+__device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, int tid) {
+    using TL = Tile<KEY_FP8, kDim>;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int piece = tid + NT * i, r = piece >> 3, p = 2 * (piece & 7);
+        const int sw = KEYS ? TL::swz_k(r) : TL::swz_v(r);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) {
+            u32x4 y;
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const uint32_t d = c.x[i][2 * o + w];
+                y[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false));
+                y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true));
+            }
+            *(u32x4 *)(dst + r * TL::ROW + 16 * ((p + o) ^ sw)) = y;
+        }
+    }
+    if (tid < 64) scales[tid] = c.scale;
+}
+
+// The page of tile `t` of request b, or -1 where it is not mapped.
+template <int FMT, int D>
+__device__ __forceinline__ int page_of(const AttendArgs &A, int b, int t) {
+    const int page = A.bt[(int64_t)b * A.bt_ld + (int64_t)t * Tile<FMT, D>::E / kPage];
+    return page >= 0 && page < A.n_phys ? page : -1;
+}
+// Where that tile starts in a pool.
+template <int FMT, int D>
+__device__ __forceinline__ int64_t tile_at(const AttendArgs &A, int page, int hk, int t) {
+    constexpr int row = FMT == KEY_FP8 ? kRowFp8 : Tile<FMT, D>::ROW;
+    return (((int64_t)page * A.n_kv + hk) * kPage + (int64_t)t * Tile<FMT, D>::E % kPage) * row;
+}
+
+// A problem's request, rows and length; the host's bounds hold whatever the device arrays say.
+struct Req {
+    int row0, n, len;
+};
+__device__ __forceinline__ Req request(const AttendArgs &A, int b) {
+    Req r;
+    r.row0 = max(0, min(A.q_start[b], A.T));
+    r.n = max(0, min(min(A.q_start[b + 1], A.T) - r.row0, A.max_rows));
+    r.len = max(0, min(A.seq_lens[b], A.max_len));
+    return r;
+}
+
+// Column outputs.  stage: D floats of each of 32 columns, row c's 16-byte piece p at p ^ (c & 15).
+template <int D>
+__device__ __forceinline__ f32x4 *stage_at(uint8_t *stage, int c, int p) {
+    return (f32x4 *)(stage + c * D * 4 + 16 * (p ^ (c & 15)));
+}
+template <int FMT, int D>
+__device__ __forceinline__ void stage_o(uint8_t *stage, const State<FMT, D> &st) {
+    const int ln = __lane_id(), j = ln & 31, h = ln >> 5;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+            const f32x4 x = {st.o[t][4 * a], st.o[t][4 * a + 1], st.o[t][4 * a + 2], st.o[t][4 * a + 3]};
+            *stage_at<D>(stage, j, 8 * t + 2 * a + h) = x;
+        }
+}
+// Writes 4 values of column R (not yet divided by l) and, from its first piece, the statistics.
+template <int FMT, int D>
+__device__ __forceinline__ void emit(const AttendArgs &A, int R, int row0, int hk, int split, int piece, f32x4 o, float m,
+                                     float l) {
+    const int64_t row = row0 + R / A.G;
+    const int head = hk * A.G + R % A.G;
+    const int64_t rh = row * A.n_heads + head;
+    if (A.splits > 1) {
+        const int64_t at = (int64_t)split * A.T * A.n_heads + rh;
+        *(f32x4 *)(A.part_o + at * D + 4 * piece) = o;
+        if (piece == 0) A.part_ml[at] = make_float2(m, l);
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if constexpr (FMT == KEY_F32) {
+        *(f32x4 *)((float *)A.out + row * A.out_ld + (int64_t)head * D + 4 * piece) = o * inv;
+    } else {
+        const u32x2 y = {pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+        *(u32x2 *)((uint16_t *)A.out + row * A.out_ld + (int64_t)head * D + 4 * piece) = y;
+    }
+    if (piece == 0 && A.lse) A.lse[rh] = l == 0.f ? kNegInf : m * A.scale + kLn2 * __builtin_amdgcn_logf(l);
+}
+
+// ------------------------------------------------------------------ few columns
+// Workgroup (split, kv head, request): its tiles are dealt to the four waves in turn.  bf16 and
+// float32 tiles are copied straight into the wave's own LDS: the next keys' copy is issued once
+// the scores are formed and the next values' once they are weighed, so each wave has one to two
+// copies in flight and waits for no other wave.  fp8 tiles are loaded a tile ahead into
+// registers.  NB: blocks of 32 columns a wave holds.
+template <int FMT, int D, int NB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(FMT == KEY_FP8 && NB == 1 ? 2 : 1)))
+void attend_split_kernel(AttendArgs A) {
+    using TL = Tile<FMT, D>;
+    constexpr bool FP8 = FMT == KEY_FP8;
+    constexpr int NI = TL::BYTES / 1024;
+    __shared__ __align__(16) uint8_t sK[4][TL::BYTES], sV[FP8 ? 1 : 4][FP8 ? 16 : TL::BYTES];
+    __shared__ float sS[FP8 ? 4 : 1][2][64], sM[4][32], sL[4][32];
+    __shared__ Special<D> sX[4][NB];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
+    const int split = blockIdx.x % A.splits, hk = (blockIdx.x / A.splits) % A.n_kv, b = blockIdx.x / (A.splits * A.n_kv);
+    const Req rq = request(A, b);
+    const int cols = rq.n * A.G;
+    if (cols == 0) return;
+    const Span sp = make_span<TL::E>(A, 0, rq.n - 1, rq.n, rq.len);
+    const int per = (sp.count + A.splits - 1) / A.splits;
+    const int t0 = split * per + w, t1 = min(sp.count, (split + 1) * per);
+    Col col[NB];
+    u32x4 q[NB][TL::QR];
+    State<FMT, D> st[NB];
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        const int R = 32 * n + j;
+        col[n] = make_col(A, R, rq.row0, rq.n, rq.len);
+        load_q<FMT, D>(q[n], A, R, rq.row0, hk, col[n].valid);
+        st[n].clear();
+        clear_special(sX[w][n]);
+    }
+    const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
+    uint8_t *kt = sK[w], *vt = FP8 ? sK[w] : sV[FP8 ? 0 : w];
+    // the next mapped tile from i on, and its page (i >= t1: none)
+    int page = -1;
+    auto seek = [&](int i) {
+        page = -1;
+        for (; i < t1; i += 4) {
+            page = __builtin_amdgcn_readfirstlane(page_of<FMT, D>(A, b, sp.at(i)));
+            if (page >= 0) break;
+        }
+        return i;
+    };
+    CodeRegs<FP8 ? 8 : 1> kc, vc;
+    auto issue_k = [&](int t) {
+        const uint8_t *src = kp + tile_at<FMT, D>(A, page, hk, t);
+        if constexpr (FP8) load_codes<8, 64>(kc, src, ln);
+        else {
+#pragma unroll
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(src, kt, n);
+        }
+    };
+    auto issue_v = [&](int t, int pg) {
+        const uint8_t *src = vp + tile_at<FMT, D>(A, pg, hk, t);
+        if constexpr (FP8) load_codes<8, 64>(vc, src, ln);
+        else {
+#pragma unroll
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(src, vt, n);
+        }
+    };
+    int i = seek(t0);
+    if (i < t1) {
+        issue_k(sp.at(i));
+        issue_v(sp.at(i), page);
+    }
+    while (i < t1) {
+        const int t = sp.at(i), s0 = t * TL::E;
+        const int nx = seek(i + 4);
+        if constexpr (FP8) {
+            put_codes<8, 64, true>(kc, kt, sS[w][0], ln);
+            __builtin_amdgcn_wave_barrier();
+        } else {
+            wait_vm<NI>();                                // the keys; the values may be in flight
+        }
+        f32x16 s[NB][TL::SUB];
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub)
+#pragma unroll
+            for (int n = 0; n < NB; ++n) s[n][sub] = scores<FMT, D>(kt, sub, q[n]);
+        __builtin_amdgcn_s_waitcnt(0xc07f);               // lgkmcnt(0): the keys are read
+        __builtin_amdgcn_sched_barrier(0);
+        if (nx < t1) issue_k(sp.at(nx));
+        if constexpr (FP8) {
+            put_codes<8, 64, false>(vc, vt, sS[w][1], ln);
+            __builtin_amdgcn_wave_barrier();
+            if (nx < t1) issue_v(sp.at(nx), page);
+        }
+        uint64_t vis[NB];
+        bool masked[NB];
+        constexpr uint64_t full = ~0ull >> (64 - TL::E);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            vis[n] = col[n].valid ? visible(col[n], s0, A.mask_ld) & full : full;
+            masked[n] = __ballot(vis[n] != full) != 0;
+            soften<FMT, D>(s[n], masked[n], vis[n], A.c, sS[FP8 ? w : 0][0], sS[FP8 ? w : 0][1], st[n]);
+        }
+        if constexpr (!FP8) {
+            if (nx < t1) wait_vm<NI>();                   // the values; the next keys may be in flight
+            else wait_vm<0>();
+        }
+#pragma unroll
+        for (int n = 0; n < NB; ++n) add_values<FMT, D>(vt, s[n], masked[n], vis[n], st[n], sX[w][n]);
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (!FP8) {
+            if (nx < t1) issue_v(sp.at(nx), page);
+        }
+        i = nx;
+    }
+    // the four waves' parts of each block of columns, joined and written by all threads
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+        if (n) __syncthreads();
+        const float l = st[n].l + other_half(st[n].l);
+        if (ln < 32) {
+            sM[w][j] = st[n].m;
+            sL[w][j] = l;
+        }
+        apply_special<FMT, D>(sX[w][n], st[n]);
+        stage_o<FMT, D>(kt, st[n]);
+        __syncthreads();
+#pragma unroll 1
+        for (int e = tid; e < 32 * (D / 4); e += 256) {
+            const int c = e / (D / 4), piece = e % (D / 4), R = 32 * n + c;
+            if (R >= cols) continue;
+            float m = kNegInf, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m = fmaxf(m, sM[k][c]);
+            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float mk = sM[k][c];
+                const float f = mk == kNegInf ? 0.f : __builtin_amdgcn_exp2f((mk - m) * A.c);
+                if (sL[k][c] == 0.f) continue;            // nothing seen
+                sum += f * sL[k][c];
+                o += f * *stage_at<D>(sK[k], c, piece);
+            }
+            emit<FMT, D>(A, R, rq.row0, hk, split, piece, o, m, sum);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ many columns
+// Workgroup (split, block of 128 columns, kv head, request).  The next tile's copy (two LDS
+// stages; fp8: registers) is in flight while a tile is worked on, one barrier a tile.
+template <int FMT, int D>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
+void attend_tile_kernel(AttendArgs A) {
+    using TL = Tile<FMT, D>;
+    constexpr bool FP8 = FMT == KEY_FP8;
+    constexpr int NI = TL::BYTES / 4096;                  // copy instructions a wave and tile
+    __shared__ __align__(16) uint8_t sK0[TL::BYTES], sV0[TL::BYTES], sK1[TL::BYTES], sV1[TL::BYTES];
+    __shared__ float sS[FP8 ? 2 : 1][2][64];
+    __shared__ Special<D> sX[4];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
+    // consecutive workgroups run on the chip's 8 XCDs in turn: each gets a contiguous run of
+    // problems, so the blocks that share a kv head's tiles share an L2, the longest first
+    const int total = gridDim.x, x = blockIdx.x % 8, per8 = total / 8, rem = total % 8;
+    int id = (x < rem ? x * (per8 + 1) : rem * (per8 + 1) + (x - rem) * per8) + blockIdx.x / 8;
+    const int split = id % A.splits;
+    id /= A.splits;
+    const int blk = A.blocks - 1 - id % A.blocks, hk = (id / A.blocks) % A.n_kv, b = id / (A.blocks * A.n_kv);
+    const Req rq = request(A, b);
+    const int cols = rq.n * A.G, c0 = blk * 128;
+    if (c0 >= cols) return;
+    const Span sp = make_span<TL::E>(A, c0 / A.G, (min(c0 + 128, cols) - 1) / A.G, rq.n, rq.len);
+    const int per = (sp.count + A.splits - 1) / A.splits;
+    const int t0 = split * per, t1 = min(sp.count, t0 + per);
+    const int R = c0 + 32 * w + j;
+    const Col col = make_col(A, R, rq.row0, rq.n, rq.len);
+    const bool idle = c0 + 32 * w >= cols;
+    u32x4 q[TL::QR];
+    load_q<FMT, D>(q, A, R, rq.row0, hk, col.valid);
+    State<FMT, D> st;
+    st.clear();
+    clear_special(sX[w]);
+    const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
+    int page = -1;
+    auto seek = [&](int i) {
+        page = -1;
+        for (; i < t1; ++i) {
+            page = __builtin_amdgcn_readfirstlane(page_of<FMT, D>(A, b, sp.at(i)));
+            if (page >= 0) break;
+        }
+        return i;
+    };
+    CodeRegs<FP8 ? 2 : 1> kc, vc;
+    auto issue = [&](uint8_t *kt, uint8_t *vt, int t) {
+        const int64_t at = tile_at<FMT, D>(A, page, hk, t);
+        if constexpr (FP8) {
+            load_codes<2, 256>(kc, kp + at, tid);
+            load_codes<2, 256>(vc, vp + at, tid);
+        } else {
+#pragma unroll
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + at, kt, NI * w + n);
+#pragma unroll
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(vp + at, vt, NI * w + n);
+        }
+    };
+    auto work = [&](const uint8_t *kt, const uint8_t *vt, const float *ks, const float *vs, int t) {
+        constexpr uint64_t full = ~0ull >> (64 - TL::E);
+        const uint64_t vis = col.valid ? visible(col, t * TL::E, A.mask_ld) & full : full;
+        if (idle || __ballot(col.valid && vis != 0) == 0) return;
+        const bool masked = __ballot(vis != full) != 0;
+        f32x16 s[TL::SUB];
+#pragma unroll
+        for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, sub, q);
+        soften<FMT, D>(s, masked, vis, A.c, ks, vs, st);
+        add_values<FMT, D>(vt, s, masked, vis, st, sX[w]);
+    };
+    int i = seek(t0);
+    // tile i is on its way to (kt, vt); after the barrier the other stage is free for the next
+    auto step = [&](uint8_t *kt, uint8_t *vt, uint8_t *kn, uint8_t *vn, int stage) {
+        const int t = sp.at(i);
+        if constexpr (FP8) {
+            put_codes<2, 256, true>(kc, kt, sS[stage][0], tid);
+            put_codes<2, 256, false>(vc, vt, sS[stage][1], tid);
+        } else {
+            wait_vm<0>();
+        }
+        __syncthreads();
+        i = seek(i + 1);
+        if (i < t1) issue(kn, vn, sp.at(i));
+        work(kt, vt, sS[FP8 ? stage : 0][0], sS[FP8 ? stage : 0][1], t);
+    };
+    if (i < t1) issue(sK0, sV0, sp.at(i));
+    while (i < t1) {
+        step(sK0, sV0, sK1, sV1, 0);
+        if (i >= t1) break;
+        step(sK1, sV1, sK0, sV0, FP8 ? 1 : 0);
+    }
+    __syncthreads();
+    uint8_t *stage = w == 0 ? sK0 : w == 1 ? sV0 : w == 2 ? sK1 : sV1;
+    const float l = st.l + other_half(st.l);
+    apply_special<FMT, D>(sX[w], st);
+    stage_o<FMT, D>(stage, st);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int e = ln; e < 32 * (D / 4); e += 64) {
+        const int c = e / (D / 4), piece = e % (D / 4);
+        const float mc = __shfl(st.m, c), lc = __shfl(l, c);
+        if (c0 + 32 * w + c < cols)
+            emit<FMT, D>(A, c0 + 32 * w + c, rq.row0, hk, split, piece, *stage_at<D>(stage, c, piece), mc, lc);
+    }
+}
+
+// ------------------------------------------------------------------ joining the parts
+// One wave a (row, head): D values, the splits' parts weighed by e^(m - max).
+template <int FMT, int D>
+__global__ __launch_bounds__(256) void attend_merge_kernel(AttendArgs A) {
+    const int ln = __lane_id();
+    const int b = blockIdx.y;
+    const Req rq = request(A, b);
+    const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int i = (int)(e / A.n_heads), head = (int)(e % A.n_heads);
+    if (i >= rq.n) return;
+    const int64_t row = rq.row0 + i, rh = row * A.n_heads + head, all = (int64_t)A.T * A.n_heads;
+    float m = kNegInf;
+    for (int s = 0; s < A.splits; ++s) {
+        const float2 x = A.part_ml[s * all + rh];
+        if (x.y != 0.f) m = fmaxf(m, x.x);
+    }
+    float l = 0.f, o[D / 64];
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) o[k] = 0.f;
+    for (int s = 0; s < A.splits; ++s) {
+        const float2 x = A.part_ml[s * all + rh];
+        if (x.y == 0.f) continue;                         // nothing seen
+        const float f = x.x == kNegInf ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * A.c);
+        l += f * x.y;
+        const float *src = A.part_o + (s * all + rh) * D;
+#pragma unroll
+        for (int k = 0; k < D / 64; ++k) o[k] += f * src[(D / 64) * ln + k];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t at = row * A.out_ld + (int64_t)head * D + (D / 64) * ln;
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) {
+        if constexpr (FMT == KEY_F32) ((float *)A.out)[at + k] = o[k] * inv;
+        else ((uint16_t *)A.out)[at + k] = (uint16_t)pack_bf16(o[k] * inv, 0.f);
+    }
+    if (ln == 0 && A.lse) A.lse[rh] = l == 0.f ? kNegInf : m * A.scale + kLn2 * __builtin_amdgcn_logf(l);
+}
+
+template <int FMT, int D>
+hipError_t launch(const AttendArgs &a, hipStream_t s) {
+    if (a.blocks) {
+        attend_tile_kernel<FMT, D><<<dim3((unsigned)(a.splits * a.blocks * a.n_kv * a.B)), 256, 0, s>>>(a);
+    } else {
+        const dim3 grid((unsigned)(a.splits * a.n_kv * a.B));
+        if (a.max_rows * a.G <= 32) attend_split_kernel<FMT, D, 1><<<grid, 256, 0, s>>>(a);
+        else attend_split_kernel<FMT, D, 2><<<grid, 256, 0, s>>>(a);
+    }
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t waves = (int64_t)a.max_rows * a.n_heads;
+    attend_merge_kernel<FMT, D><<<dim3((unsigned)((waves + 3) / 4), (unsigned)a.B), 256, 0, s>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int attend_tile_entries(int key_fmt) { return key_fmt == KEY_F32 ? 32 : 64; }
+
+hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s) {
+    if (key_fmt == KEY_F32) return head_dim == 64 ? launch<KEY_F32, 64>(a, s) : launch<KEY_F32, 128>(a, s);
+    if (key_fmt == KEY_BF16) return head_dim == 64 ? launch<KEY_BF16, 64>(a, s) : launch<KEY_BF16, 128>(a, s);
+    return launch<KEY_FP8, kDim>(a, s);
+}
+
+}  // namespace fm

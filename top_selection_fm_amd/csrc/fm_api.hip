@@ -57,12 +57,11 @@ fm_status launched(hipError_t e, const char *what) {
     return FM_OK;
 }
 
-fm_status check_kv(const fm_kv_desc *kv, int n_pools_needed) {
+// The parts of a cache descriptor that do not depend on what its rows hold.
+fm_status check_pages(const fm_kv_desc *kv, int n_pools_needed) {
     REQUIRE(kv, FM_ERR_INVALID_ARG, "kv descriptor is NULL");
     REQUIRE(kv->page_size == FM_PAGE_SIZE, FM_ERR_UNSUPPORTED, "page_size %d (only %d)",
             kv->page_size, FM_PAGE_SIZE);
-    REQUIRE(kv->head_dim == FM_HEAD_DIM, FM_ERR_UNSUPPORTED, "head_dim %d (only %d)",
-            kv->head_dim, FM_HEAD_DIM);
     REQUIRE(kv->key_dtype == FM_F32 || kv->key_dtype == FM_BF16 ||
                 kv->key_dtype == FM_FP8_E4M3_SCALED132,
             FM_ERR_UNSUPPORTED, "key dtype %d", (int)kv->key_dtype);
@@ -80,6 +79,23 @@ fm_status check_kv(const fm_kv_desc *kv, int n_pools_needed) {
             FM_ERR_INVALID_ARG, "bt_ld = %lld < ceil(max_seq_len / 64)", (long long)kv->bt_ld);
     REQUIRE(kv->n_phys_pages >= 1 && kv->n_phys_pages <= (int64_t)INT32_MAX, FM_ERR_INVALID_ARG,
             "n_phys_pages = %lld", (long long)kv->n_phys_pages);
+    return FM_OK;
+}
+
+fm_status check_kv(const fm_kv_desc *kv, int n_pools_needed) {
+    REQUIRE(!kv || kv->page_size != FM_PAGE_SIZE || kv->head_dim == FM_HEAD_DIM, FM_ERR_UNSUPPORTED,
+            "head_dim %d (only %d)", kv->head_dim, FM_HEAD_DIM);
+    return check_pages(kv, n_pools_needed);
+}
+
+// A cache of key and value pools for attention: head_dim 64 or 128, 132-byte rows 128 only.
+fm_status check_kv_pairs(const fm_kv_desc *kv, int layer) {
+    REQUIRE(layer >= 0 && layer < FM_MAX_POOLS / 2, FM_ERR_INVALID_ARG, "layer = %d", layer);
+    CHECK(check_pages(kv, 2 * layer + 2));
+    REQUIRE(kv->head_dim == 64 || kv->head_dim == 128, FM_ERR_UNSUPPORTED, "head_dim %d (64 or 128)",
+            kv->head_dim);
+    REQUIRE(kv->key_dtype != FM_FP8_E4M3_SCALED132 || kv->head_dim == 128, FM_ERR_UNSUPPORTED,
+            "132-byte rows hold 128 values, head_dim is %d", kv->head_dim);
     return FM_OK;
 }
 
@@ -475,9 +491,139 @@ void yarn_freqs(const fm_encoder_desc *e, double *out) {
     }
 }
 
+// ---------------------------------------------------------------- attention
+int clamp32(int64_t x) { return (int)std::min<int64_t>(x, INT32_MAX); }
+
+fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
+    REQUIRE(a, FM_ERR_INVALID_ARG, "attention descriptor is NULL");
+    CHECK(check_kv_pairs(kv, a->layer));
+    const fm_dtype k = kv->key_dtype;
+    REQUIRE((a->q_dtype == FM_F32 && k == FM_F32) ||
+                (a->q_dtype == FM_BF16 && (k == FM_BF16 || k == FM_FP8_E4M3_SCALED132)),
+            FM_ERR_UNSUPPORTED, "q dtype %d with key dtype %d", (int)a->q_dtype, (int)k);
+    REQUIRE(a->T >= 0 && a->max_rows >= 0, FM_ERR_INVALID_ARG, "T = %d, max_rows = %d", a->T, a->max_rows);
+    REQUIRE(a->n_kv_heads >= 1 && a->n_heads >= 1 && a->n_heads % a->n_kv_heads == 0, FM_ERR_INVALID_ARG,
+            "n_heads = %d, n_kv_heads = %d", a->n_heads, a->n_kv_heads);
+    REQUIRE(a->n_heads <= 1024, FM_ERR_UNSUPPORTED, "n_heads = %d (at most 1024)", a->n_heads);
+    REQUIRE(a->scale > 0.f && a->scale < INFINITY, FM_ERR_INVALID_ARG, "scale = %g", (double)a->scale);
+    REQUIRE(window >= 1 && n_sink >= 0, FM_ERR_INVALID_ARG, "window = %lld, n_sink = %lld",
+            (long long)window, (long long)n_sink);
+    const int64_t row = (int64_t)a->n_heads * kv->head_dim, unit = a->q_dtype == FM_F32 ? 4 : 8;
+    REQUIRE(a->q_ld >= row && a->out_ld >= row && a->q_ld % unit == 0 && a->out_ld % unit == 0,
+            FM_ERR_INVALID_ARG, "q_ld = %lld, out_ld = %lld (at least %lld, multiples of 16 bytes)",
+            (long long)a->q_ld, (long long)a->out_ld, (long long)row);
+    // columns of a problem and workgroups are counted in 32 bits
+    REQUIRE((int64_t)a->max_rows * a->n_heads < (1 << 30) &&
+                ((int64_t)a->max_rows * a->n_heads / 128 + a->n_heads) * kv->B < (1 << 25),
+            FM_ERR_UNSUPPORTED, "max_rows = %d with %d heads and %d requests", a->max_rows, a->n_heads, kv->B);
+    if (a->T == 0 || a->max_rows == 0) return FM_OK;
+    REQUIRE(a->q && a->out && a->q_start, FM_ERR_INVALID_ARG, "q / out / q_start NULL");
+    REQUIRE(aligned(a->q, 16) && aligned(a->out, 16), FM_ERR_INVALID_ARG, "q / out not 16-byte aligned");
+    REQUIRE(aligned(a->lse, 4), FM_ERR_INVALID_ARG, "lse not 4-byte aligned");
+    return FM_OK;
+}
+
+// The kernel and the split of the entries: up to 64 columns (rows x heads of a kv head) take the
+// kernel whose waves stream tiles of their own, more take 128-column blocks.  Entries are split
+// over more workgroups while there are fewer than kAttendTarget and each keeps kAttendMinTiles.
+#ifndef FM_ATTEND_TARGET
+#define FM_ATTEND_TARGET 512
+#endif
+#ifndef FM_ATTEND_MIN_TILES
+#define FM_ATTEND_MIN_TILES 8
+#endif
+struct AttendPlan {
+    int blocks, splits;
+    size_t ml_bytes, o_bytes;
+};
+AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
+    AttendPlan p{0, 1, 0, 0};
+    if (a->T == 0 || a->max_rows == 0) return p;
+    const int G = a->n_heads / a->n_kv_heads;
+    const int64_t cols = (int64_t)a->max_rows * G;
+    p.blocks = cols <= 64 ? 0 : (int)((cols + 127) / 128);
+    const int64_t rows = std::min<int64_t>(a->max_rows, (p.blocks ? 128 : 64) / G + 2);
+    const int E = fm::attend_tile_entries(key_fmt(kv->key_dtype));
+    const int64_t seen = std::min<int64_t>(std::min<int64_t>(window, kv->max_seq_len) + rows +
+                                               std::min<int64_t>(n_sink, kv->max_seq_len), kv->max_seq_len);
+    const int64_t tiles = (seen + E - 1) / E;
+    const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
+    const int64_t want = (FM_ATTEND_TARGET + wgs - 1) / wgs;
+    p.splits = (int)std::max<int64_t>(1, std::min(want, tiles / FM_ATTEND_MIN_TILES));
+    if (p.splits > 1) {
+        const size_t parts = (size_t)p.splits * a->T * a->n_heads;
+        p.ml_bytes = fm::align_up(parts * sizeof(float2), 256);
+        p.o_bytes = parts * kv->head_dim * sizeof(float);
+    }
+    return p;
+}
+
+fm_status run_attend(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t *tree_mask, int64_t mask_ld,
+                     int64_t window, int64_t n_sink, void *ws, size_t ws_bytes, void *stream) {
+    if (a->T == 0 || a->max_rows == 0) return ok();
+    const AttendPlan p = attend_plan(a, kv, window, n_sink);
+    const size_t need = p.ml_bytes + p.o_bytes;
+    REQUIRE(need == 0 || (ws && aligned(ws, 256) && ws_bytes >= need), FM_ERR_WORKSPACE,
+            "workspace %zu bytes at %p, need %zu (256-byte aligned)", ws_bytes, ws, need);
+    fm::AttendArgs x;
+    x.q = a->q;
+    x.q_ld = a->q_ld;
+    x.out = a->out;
+    x.out_ld = a->out_ld;
+    x.lse = a->lse;
+    x.q_start = a->q_start;
+    x.T = a->T;
+    x.B = kv->B;
+    x.max_rows = std::min(a->max_rows, a->T);
+    x.n_heads = a->n_heads;
+    x.n_kv = a->n_kv_heads;
+    x.G = a->n_heads / a->n_kv_heads;
+    x.scale = a->scale;
+    x.c = (float)((double)a->scale * M_LOG2E);
+    x.k = kv->pool[2 * a->layer];
+    x.v = kv->pool[2 * a->layer + 1];
+    x.bt = kv->block_table;
+    x.bt_ld = kv->bt_ld;
+    x.seq_lens = kv->seq_lens;
+    x.n_phys = kv->n_phys_pages;
+    x.max_len = (int)kv->max_seq_len;
+    x.window = clamp32(window);
+    x.n_sink = clamp32(n_sink);
+    x.tree_mask = tree_mask;
+    x.mask_ld = mask_ld;
+    x.blocks = p.blocks;
+    x.splits = p.splits;
+    x.part_ml = (float2 *)ws;
+    x.part_o = (float *)((uint8_t *)ws + p.ml_bytes);
+    CHECK(launched(fm::launch_attend(x, key_fmt(kv->key_dtype), kv->head_dim, (hipStream_t)stream), "attention"));
+    return ok();
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t fm_attend_workspace_bytes(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
+    if (check_attend(a, kv, window, n_sink) != FM_OK) return 0;
+    const AttendPlan p = attend_plan(a, kv, window, n_sink);
+    return p.ml_bytes + p.o_bytes;
+}
+
+fm_status fm_attend_window(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink, void *ws,
+                           size_t ws_bytes, void *stream) {
+    CHECK(check_attend(a, kv, window, n_sink));
+    return run_attend(a, kv, nullptr, 0, window, n_sink, ws, ws_bytes, stream);
+}
+
+fm_status fm_attend_tree(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t *tree_mask, int64_t mask_ld,
+                         int64_t window, int64_t n_sink, void *ws, size_t ws_bytes, void *stream) {
+    CHECK(check_attend(a, kv, window, n_sink));
+    REQUIRE(mask_ld >= 1 && a->max_rows <= 64 * std::min<int64_t>(mask_ld, 1 << 24), FM_ERR_INVALID_ARG,
+            "mask_ld = %lld words for up to %d drafts", (long long)mask_ld, a->max_rows);
+    REQUIRE(a->T == 0 || (tree_mask && aligned(tree_mask, 8)), FM_ERR_INVALID_ARG,
+            "tree_mask NULL or not 8-byte aligned");
+    return run_attend(a, kv, tree_mask, mask_ld, window, n_sink, ws, ws_bytes, stream);
+}
 
 fm_status fm_index_logits(const fm_query_desc *q, const fm_kv_desc *kv, float *logits,
                           int64_t ld, void *stream) {

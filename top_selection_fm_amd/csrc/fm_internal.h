@@ -233,6 +233,34 @@ size_t labels_ws_bytes(int T, int n_layers, int64_t ld, int tau);
 void labels_ws_carve(LabelArgs &a, void *ws);
 hipError_t launch_labels(const LabelArgs &a, hipStream_t s);
 
+// Attention over paged keys and values (attend.hip).
+struct AttendArgs {
+    const void *q;            // [T, n_heads, D], rows q_ld elements apart
+    int64_t q_ld;
+    void *out;                // the query type, rows out_ld elements apart
+    int64_t out_ld;
+    float *lse;               // [T, n_heads] or null
+    const int32_t *q_start;   // [B + 1]
+    int T, B, max_rows;
+    int n_heads, n_kv, G;     // G = n_heads / n_kv
+    float scale, c;           // score scale, and scale * log2 e
+    const void *k, *v;        // pools [n_phys, n_kv, 64, row]
+    const int32_t *bt;
+    int64_t bt_ld;
+    const int32_t *seq_lens;
+    int64_t n_phys;
+    int max_len;
+    int window, n_sink;       // entries back from a row's own (itself included); first entries
+    const uint64_t *tree_mask;   // [T, mask_ld] or null
+    int64_t mask_ld;
+    int blocks;               // 128-column blocks of a problem (tile kernel); 0: split kernel
+    int splits;               // parts the entries are split into
+    float *part_o;            // [splits, T, n_heads, D]
+    float2 *part_ml;          // [splits, T, n_heads]: maximum, sum
+};
+int attend_tile_entries(int key_fmt);
+hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s);
+
 size_t topk_ws_bytes(int T, int64_t n);   // bytes for T rows of up to n entries (0: not used)
 TopkWs topk_ws_carve(void *ws, int T, int64_t n);
 
