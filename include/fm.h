@@ -445,6 +445,128 @@ fm_status fm_attend_tree(const fm_attn_desc *a, const fm_kv_desc *kv, const uint
                          int64_t mask_ld, int64_t window, int64_t n_sink, void *ws,
                          size_t ws_bytes, void *stream);
 
+/*
+ * Norms of queries and keys for each head, the position rotation in the same pass, and the keys
+ * and values written into a cache (README, "Retriever architecture": the encoder's RMSNorm and
+ * YaRN RoPE, here per head and with the store).  For every row t and head of q (n_heads) and k
+ * (n_kv_heads), x of head_dim values:
+ *   y = x / sqrt(mean(x^2) + rms_eps) * q_norm (k_norm); a NULL weight leaves that side un-normed;
+ *   the dims rope_first .. rope_first + rope_dim - 1 of y turn by pos[t] * theta_i (theta as in
+ *   fm_encoder_desc), pairs being the dims (2 i, 2 i + 1) of that range, or with rope_halves
+ *   (i, i + rope_dim / 2).
+ * q' goes to q_out, k' to k_out (nullable) and, with a cache, k' and the untouched v to entry
+ * slot[t] (NULL: pos[t]) of request row_req[t] (NULL: row t is request t when T == B, or request
+ * 0 when B == 1) in pools 2 layer and 2 layer + 1.  A row whose request is out of range, whose
+ * slot is not in [0, seq_lens[b]) or whose page is not mapped is not stored.  Two rows with the
+ * same entry: one of the two, piece by piece.  The arithmetic is float32 (the angle float64), with one rounding at
+ * each store; 132-byte rows take scale = max |x| / 448 (1 for a row of zeros) and the nearest
+ * E4M3FN codes of x / scale.  Inputs are finite.
+ * Rows are ld elements apart (>= heads * head_dim, a multiple of 16 bytes) and 16-byte aligned, as
+ * are the weights, of the inputs' type; q_out may be q and k_out may be k where the ld is the same.
+ * dtype F32 goes with F32 pools, BF16 with BF16 or SCALED132 ones.  kv NULL: no cache, v is not
+ * read and k_out is needed.  rope_dim 0: no rotation.  rope_first is even; with rope_halves
+ * rope_first and rope_dim / 2 are multiples of 8.  No workspace; T = 0 is a no-op.
+ */
+typedef struct {
+    const void *q, *k, *v;
+    int64_t q_ld, k_ld, v_ld;
+    void *q_out, *k_out;
+    int64_t q_out_ld, k_out_ld;
+    const void *q_norm, *k_norm;
+    fm_dtype dtype;             /* of q, k, v, the outputs and the weights: FM_F32 or FM_BF16 */
+    int T;                      /* <= 2^22 */
+    int n_heads, n_kv_heads;    /* either may be 0 */
+    int head_dim;               /* 64 or 128 */
+    const int32_t *pos;         /* [T] */
+    const int32_t *row_req;     /* [T] or NULL */
+    const int32_t *slot;        /* [T] or NULL */
+    int layer;
+    float rms_eps;              /* >= 0 */
+    int rope_dim, rope_first;   /* even, rope_first + rope_dim <= head_dim */
+    int rope_halves;            /* 0 or 1 */
+    float rope_base;            /* > 1 */
+    float rope_factor;          /* >= 1; 1: plain RoPE */
+    int rope_orig_len;          /* > 0 */
+    float beta_fast, beta_slow; /* beta_fast > beta_slow > 0 */
+} fm_qk_desc;
+
+fm_status fm_qk_norm_rope(const fm_qk_desc *d, const fm_kv_desc *kv, void *stream);
+
+/*
+ * ---- the pages of a cache -----------------------------------------------------------------------
+ *
+ * Pools that share one block table (the compressed-key pools of an fm_kv_desc, key/value pools, or
+ * both), with the state that says which pages are whose, all in device memory and owned by the
+ * caller:
+ *   pool[l]       [n_phys_pages][heads[l]][64][row_bytes[l]], 16-byte aligned, row_bytes a multiple of 4
+ *   block_table   [B, bt_ld]; the first ceil(seq_lens[b] / 64) cells of a row are in use (-1: no page)
+ *   ref           [n_phys_pages]: cells in use that name the page; 0: free
+ *   free_list     [n_phys_pages], n_free [1]: the free pages are free_list[0 .. n_free - 1], taken
+ *                 from the end
+ * A new cache has seq_lens and ref all 0, free_list a permutation of the pages, n_free = n_phys_pages.
+ * The calls below keep these in step, on the device alone (they can be captured); calls on one
+ * cache must not overlap in time.  Each takes n entries (one request each, listed on the device)
+ * and writes ok[i] (nullable) = 1 for an entry carried out, 0 for one refused, which changes
+ * nothing.  Refused are requests out of range, a request named by an earlier entry of the same
+ * call, and what each call says.  Results do not depend on timing: pages are taken in list order
+ * and given back in page order.  n = 0 is a no-op.  Limits: B and n <= 16,384, n_phys_pages <= 524,288.
+ */
+typedef struct {
+    void *pool[FM_MAX_POOLS];
+    int heads[FM_MAX_POOLS];
+    int row_bytes[FM_MAX_POOLS];
+    int n_pools;
+    int32_t *block_table;
+    int64_t bt_ld;
+    int32_t *seq_lens;
+    int B;
+    int32_t *ref;
+    int32_t *free_list;
+    int32_t *n_free;
+    int64_t n_phys_pages;
+} fm_cache_desc;
+
+/* Workspace bytes of fm_cache_fork and fm_cache_grow for n entries. */
+size_t fm_cache_workspace_bytes(const fm_cache_desc *c, int n);
+
+/*
+ * Request dst[i] (of length 0) becomes a copy of request src[i] as it was before the call.  Full
+ * pages are shared (one reference more); a last page that is only partly filled is copied, so
+ * both can go on writing.  deep: every page is copied.  Refused: src[i] == dst[i], dst[i] not of
+ * length 0, and, once the pages needed by the valid entries 0 .. i exceed the free ones, entry i
+ * (and so every valid one after it).
+ */
+fm_status fm_cache_fork(const fm_cache_desc *c, const int32_t *src, const int32_t *dst, int n,
+                        int deep, int32_t *ok, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Request req[i] gets pages for new_len[i] >= its length entries (the new ones' contents are not
+ * set) and that length.  A partly filled last page that others share is copied first, so the new
+ * entries are this request's own.  Refused: a shorter length, one past 64 bt_ld, and, as above,
+ * entries for which the pages do not suffice.
+ */
+fm_status fm_cache_grow(const fm_cache_desc *c, const int32_t *req, const int32_t *new_len, int n,
+                        int32_t *ok, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Request req[i] is cut to new_len[i] entries (new_len NULL: 0, the request ends).  Cells past the
+ * new length become -1, each page in them loses a reference and, with the last, is free again.
+ * Refused: a length that is negative or more than the request has.  No workspace.
+ */
+fm_status fm_cache_free(const fm_cache_desc *c, const int32_t *req, const int32_t *new_len, int n,
+                        int32_t *ok, void *stream);
+
+/*
+ * Of request req[i]'s entries from start[i] on, the n_keep[i] listed in keep[i * keep_ld ..]
+ * (ascending entries) move to start[i], start[i] + 1, .. in every pool, and the request is cut
+ * behind them as by fm_cache_free: the accepted path of a drafted tree, or what an eviction
+ * leaves.  In place: refused are lists that are not strictly ascending within [start, length), and
+ * those where a page that receives a moved entry is shared or a page is not mapped.  No workspace.
+ */
+fm_status fm_cache_compact(const fm_cache_desc *c, const int32_t *req, const int32_t *start,
+                           const int32_t *keep, int64_t keep_ld, const int32_t *n_keep, int n,
+                           int32_t *ok, void *stream);
+
 /* Static description of a status code. */
 const char *fm_status_string(fm_status s);
 

@@ -31,7 +31,8 @@ EXPORTS = ["fm_index_logits", "fm_index_topk", "fm_resident_mask", "fm_topk512",
            "fm_score_resident_noalloc", "fm_score_resident_cells", "fm_densest_pages", "fm_workspace_bytes",
            "fm_encode_queries", "fm_encode_workspace_bytes", "fm_golden_labels",
            "fm_golden_workspace_bytes", "fm_attend_workspace_bytes", "fm_attend_window", "fm_attend_tree",
-           "fm_status_string", "fm_last_error", "fm_version"]
+           "fm_qk_norm_rope", "fm_cache_workspace_bytes", "fm_cache_fork", "fm_cache_grow", "fm_cache_free",
+           "fm_cache_compact",           "fm_status_string", "fm_last_error", "fm_version"]
 
 
 class FmError(RuntimeError):
@@ -69,6 +70,24 @@ class AttnDesc(C.Structure):
                 ("scale", C.c_float), ("layer", C.c_int)]
 
 
+class QkDesc(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("q", "k", "v")] + [(n, C.c_int64) for n in ("q_ld", "k_ld", "v_ld")] +
+                [(n, C.c_void_p) for n in ("q_out", "k_out")] + [(n, C.c_int64) for n in ("q_out_ld", "k_out_ld")] +
+                [(n, C.c_void_p) for n in ("q_norm", "k_norm")] +
+                [(n, C.c_int) for n in ("dtype", "T", "n_heads", "n_kv_heads", "head_dim")] +
+                [(n, C.c_void_p) for n in ("pos", "row_req", "slot")] +
+                [("layer", C.c_int), ("rms_eps", C.c_float), ("rope_dim", C.c_int), ("rope_first", C.c_int),
+                 ("rope_halves", C.c_int), ("rope_base", C.c_float), ("rope_factor", C.c_float),
+                 ("rope_orig_len", C.c_int), ("beta_fast", C.c_float), ("beta_slow", C.c_float)])
+
+
+class CacheDesc(C.Structure):
+    _fields_ = [("pool", C.c_void_p * FM_MAX_POOLS), ("heads", C.c_int * FM_MAX_POOLS),
+                ("row_bytes", C.c_int * FM_MAX_POOLS), ("n_pools", C.c_int), ("block_table", C.c_void_p),
+                ("bt_ld", C.c_int64), ("seq_lens", C.c_void_p), ("B", C.c_int), ("ref", C.c_void_p),
+                ("free_list", C.c_void_p), ("n_free", C.c_void_p), ("n_phys_pages", C.c_int64)]
+
+
 _lib = None
 
 
@@ -101,9 +120,18 @@ def lib():
         L.fm_attend_workspace_bytes.restype = C.c_size_t
         L.fm_attend_window.argtypes = [P, P, I64, I64, P, C.c_size_t, P]
         L.fm_attend_tree.argtypes = [P, P, P, I64, I64, I64, P, C.c_size_t, P]
+        L.fm_qk_norm_rope.argtypes = [P, P, P]
+        SZ = C.c_size_t
+        L.fm_cache_workspace_bytes.argtypes = [P, C.c_int]
+        L.fm_cache_workspace_bytes.restype = SZ
+        L.fm_cache_fork.argtypes = [P, P, P, C.c_int, C.c_int, P, P, SZ, P]
+        L.fm_cache_grow.argtypes = [P, P, P, C.c_int, P, P, SZ, P]
+        L.fm_cache_free.argtypes = [P, P, P, C.c_int, P, P]
+        L.fm_cache_compact.argtypes = [P, P, P, P, I64, P, C.c_int, P, P]
         for f in ("fm_index_logits", "fm_index_topk", "fm_resident_mask", "fm_topk512", "fm_score_resident",
                   "fm_score_resident_noalloc", "fm_score_resident_cells", "fm_densest_pages", "fm_encode_queries",
-                  "fm_golden_labels", "fm_attend_window", "fm_attend_tree"):
+                  "fm_golden_labels", "fm_attend_window", "fm_attend_tree",
+                  "fm_qk_norm_rope", "fm_cache_fork", "fm_cache_grow", "fm_cache_free", "fm_cache_compact"):
             getattr(L, f).restype = C.c_int
         L.fm_workspace_bytes.argtypes = [C.c_int, C.c_int, I64]
         L.fm_workspace_bytes.restype = C.c_size_t
@@ -260,18 +288,53 @@ def fm_encode_queries(desc: EncoderDesc, hidden, T: int, pos, q, w, ws, ws_bytes
                                    _ptr(w), _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
+def _heads(t, name: str) -> tuple:
+    """(pointer, row stride, rows, heads, head_dim) of [T, heads, head_dim] with packed heads."""
+    if t is None:
+        return None, 0, 0, 0, 0
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"{name} is [T, heads, head_dim] with packed heads")
+    T, H, D = t.shape
+    return _ptr(t), t.stride(0) if T > 1 else H * D, T, H, D
+
+
+def qk_desc(q, k, v, dtype: str, q_out, q_norm, k_norm, pos, *, k_out=None, row_req=None, slot=None,
+            layer: int = 0, rms_eps: float = 1e-6, rope_dim: int = 64, rope_first: int | None = None,
+            rope_halves: bool = False, rope_base: float = 160000.0, rope_factor: float = 16.0,
+            rope_orig_len: int = 65536, beta_fast: float = 32.0, beta_slow: float = 1.0) -> QkDesc:
+    """fm_qk_desc over q [T, n_heads, head_dim] and k, v [T, n_kv_heads, head_dim]; rows may be
+    strided.  The rotated dims are the last rope_dim ones unless rope_first says otherwise."""
+    (qp, ql, Tq, H, Dq), (kp, kl, Tk, K, Dk) = _heads(q, "q"), _heads(k, "k")
+    vp, vl, Tv, Kv, Dv = _heads(v, "v")
+    T, D = (Tq, Dq) if q is not None else (Tk, Dk)
+    if (k is not None and (Tk, Dk) != (T, D)) or (v is not None and (Tv, Kv, Dv) != (T, K, D)):
+        raise ValueError("q, k and v differ in rows, heads or head_dim")
+    qo, qol, ko, kol = *_heads(q_out, "q_out")[:2], *_heads(k_out, "k_out")[:2]
+    if (q_out is not None and q_out.shape != q.shape) or (k_out is not None and k_out.shape != k.shape):
+        raise ValueError("an output differs from its input in shape")
+    d = QkDesc(qp, kp, vp, ql, kl, vl, qo, ko, qol, kol, _ptr(q_norm), _ptr(k_norm), Q_DTYPES[dtype], T, H, K, D,
+                  _ptr(pos), _ptr(row_req), _ptr(slot), int(layer), float(rms_eps), int(rope_dim),
+                  int(D - rope_dim if rope_first is None else rope_first), int(rope_halves), float(rope_base),
+                  float(rope_factor), int(rope_orig_len), float(beta_fast), float(beta_slow))
+    d.tensors = (q, k, v, q_out, q_norm, k_norm, pos, k_out, row_req, slot)    # alive while the descriptor is
+    return d
+
+
+def fm_qk_norm_rope(d: QkDesc, kv: KvDesc | None, stream=None) -> None:
+    _check(lib().fm_qk_norm_rope(C.byref(d), None if kv is None else C.byref(kv), _stream(stream)))
+
+
 def attn_desc(q, q_dtype: str, out, q_start, max_rows: int, *, n_kv_heads: int, scale: float, lse=None,
               layer: int = 0) -> AttnDesc:
     """fm_attn_desc over q and out [T, n_heads, head_dim] (rows may be strided, heads packed)."""
-    for t in (q, out):
-        if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            raise ValueError("q and out are [T, n_heads, head_dim] with packed heads")
     if q.shape != out.shape:
         raise ValueError("q and out differ in shape")
-    T, H, D = q.shape
-    return AttnDesc(_ptr(q), Q_DTYPES[q_dtype], q.stride(0) if T > 1 else H * D, _ptr(out),
-                    out.stride(0) if T > 1 else H * D, _ptr(lse), _ptr(q_start), T, int(max_rows), H,
-                    int(n_kv_heads), float(scale), int(layer))
+    qp, ql, T, H, _ = _heads(q, "q")
+    op, ol = _heads(out, "out")[:2]
+    d = AttnDesc(qp, Q_DTYPES[q_dtype], ql, op, ol, _ptr(lse), _ptr(q_start), T, int(max_rows), H,
+                 int(n_kv_heads), float(scale), int(layer))
+    d.tensors = (q, out, lse, q_start)                  # alive while the descriptor is
+    return d
 
 
 def fm_attend_workspace_bytes(a: AttnDesc, kv: KvDesc, window: int, n_sink: int) -> int:
@@ -288,6 +351,50 @@ def fm_attend_tree(a: AttnDesc, kv: KvDesc, tree_mask, mask_ld: int, window: int
                    ws_bytes: int = 0, stream=None) -> None:
     _check(lib().fm_attend_tree(C.byref(a), C.byref(kv), _ptr(tree_mask), int(mask_ld), int(window), int(n_sink),
                                 _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def cache_desc(pools, block_table, seq_lens, ref, free_list, n_free) -> CacheDesc:
+    """fm_cache_desc over pools [pages, heads, 64, row] (any type; [pages, 64, row]: one head)."""
+    d = CacheDesc()
+    for i, p in enumerate(pools):
+        if not p.is_contiguous() or p.shape[-2] != PAGE or p.shape[0] != ref.shape[0]:
+            raise ValueError("pools are contiguous [pages, heads, 64, row] arrays of as many pages as ref")
+        d.pool[i] = _ptr(p)
+        d.heads[i] = p.shape[1] if p.dim() == 4 else 1
+        d.row_bytes[i] = p.shape[-1] * p.element_size()
+    d.n_pools = len(pools)
+    d.block_table = _ptr(block_table)
+    d.bt_ld = block_table.shape[1]
+    d.seq_lens = _ptr(seq_lens)
+    d.B = seq_lens.shape[0]
+    d.ref, d.free_list, d.n_free = _ptr(ref), _ptr(free_list), _ptr(n_free)
+    d.n_phys_pages = ref.shape[0]
+    d.tensors = (*pools, block_table, seq_lens, ref, free_list, n_free)    # alive while the descriptor is
+    return d
+
+
+def fm_cache_workspace_bytes(c: CacheDesc, n: int) -> int:
+    return int(lib().fm_cache_workspace_bytes(C.byref(c), int(n)))
+
+
+def fm_cache_fork(c: CacheDesc, src, dst, n: int, deep: bool = False, ok=None, ws=None, ws_bytes: int = 0,
+                  stream=None) -> None:
+    _check(lib().fm_cache_fork(C.byref(c), _ptr(src), _ptr(dst), int(n), int(deep), _ptr(ok), _ptr(ws), int(ws_bytes),
+                               _stream(stream)))
+
+
+def fm_cache_grow(c: CacheDesc, req, new_len, n: int, ok=None, ws=None, ws_bytes: int = 0, stream=None) -> None:
+    _check(lib().fm_cache_grow(C.byref(c), _ptr(req), _ptr(new_len), int(n), _ptr(ok), _ptr(ws), int(ws_bytes),
+                               _stream(stream)))
+
+
+def fm_cache_free(c: CacheDesc, req, new_len, n: int, ok=None, stream=None) -> None:
+    _check(lib().fm_cache_free(C.byref(c), _ptr(req), _ptr(new_len), int(n), _ptr(ok), _stream(stream)))
+
+
+def fm_cache_compact(c: CacheDesc, req, start, keep, keep_ld: int, n_keep, n: int, ok=None, stream=None) -> None:
+    _check(lib().fm_cache_compact(C.byref(c), _ptr(req), _ptr(start), _ptr(keep), int(keep_ld), _ptr(n_keep), int(n),
+                                  _ptr(ok), _stream(stream)))
 
 
 def fm_golden_workspace_bytes(T: int, n_layers: int, ld: int, tau: int) -> int:

@@ -469,7 +469,8 @@ EncPlan enc_plan(const fm_encoder_desc *e, int T) {
 // YaRN per-pair frequencies: theta_i = base^(-2i/d), divided by the factor above the slow
 // correction dim, kept below the fast one, blended linearly in between.  The correction dim of
 // beta is the pair index whose wavelength fits beta times into the original context.
-void yarn_freqs(const fm_encoder_desc *e, double *out) {
+template <class Desc>     // fm_encoder_desc or fm_qk_desc
+void yarn_freqs(const Desc *e, double *out) {
     const int d = e->rope_dim, half = d / 2;
     const double base = e->rope_base, f = e->rope_factor;
     auto corr = [&](double beta) {
@@ -489,6 +490,111 @@ void yarn_freqs(const fm_encoder_desc *e, double *out) {
         ramp = ramp < 0 ? 0 : ramp > 1 ? 1 : ramp;
         out[i] = th / f * ramp + th * (1.0 - ramp);
     }
+}
+
+// ---------------------------------------------------------------- pages of a cache
+fm_status check_cache(const fm_cache_desc *c, int n) {
+    REQUIRE(c, FM_ERR_INVALID_ARG, "cache descriptor is NULL");
+    REQUIRE(n >= 0, FM_ERR_INVALID_ARG, "n = %d", n);
+    REQUIRE(c->B >= 1 && c->bt_ld >= 1 && c->bt_ld <= INT32_MAX / FM_PAGE_SIZE && c->n_phys_pages >= 1,
+            FM_ERR_INVALID_ARG, "B = %d, bt_ld = %lld, n_phys_pages = %lld", c->B, (long long)c->bt_ld,
+            (long long)c->n_phys_pages);
+    REQUIRE(c->B <= fm::kCacheMaxRequests && n <= fm::kCacheMaxRequests && c->n_phys_pages <= fm::kCacheMaxPages,
+            FM_ERR_UNSUPPORTED, "B = %d, n = %d (at most %d), n_phys_pages = %lld (at most %d)", c->B, n,
+            fm::kCacheMaxRequests, (long long)c->n_phys_pages, fm::kCacheMaxPages);
+    REQUIRE(c->n_pools >= 1 && c->n_pools <= FM_MAX_POOLS, FM_ERR_INVALID_ARG, "n_pools = %d (1..%d)", c->n_pools,
+            FM_MAX_POOLS);
+    for (int l = 0; l < c->n_pools; ++l) {
+        REQUIRE(c->pool[l] && aligned(c->pool[l], 16), FM_ERR_INVALID_ARG, "pool[%d] NULL or not 16-byte aligned", l);
+        REQUIRE(c->heads[l] >= 1 && c->heads[l] <= 1024 && c->row_bytes[l] >= 4 && c->row_bytes[l] <= (1 << 16) &&
+                    c->row_bytes[l] % 4 == 0,
+                FM_ERR_INVALID_ARG, "pool[%d]: %d heads of %d-byte rows", l, c->heads[l], c->row_bytes[l]);
+    }
+    REQUIRE(c->block_table && c->seq_lens && c->ref && c->free_list && c->n_free, FM_ERR_INVALID_ARG,
+            "block_table / seq_lens / ref / free_list / n_free NULL");
+    return FM_OK;
+}
+
+fm::CacheArgs make_cache(const fm_cache_desc *c, int n) {
+    fm::CacheArgs a = {};
+    for (int l = 0; l < c->n_pools; ++l) {
+        a.pool[l] = (uint8_t *)c->pool[l];
+        a.heads[l] = c->heads[l];
+        a.row_bytes[l] = c->row_bytes[l];
+    }
+    a.n_pools = c->n_pools;
+    a.block_table = c->block_table;
+    a.bt_ld = c->bt_ld;
+    a.seq_lens = c->seq_lens;
+    a.B = c->B;
+    a.ref = c->ref;
+    a.free_list = c->free_list;
+    a.n_free = c->n_free;
+    a.n_phys = c->n_phys_pages;
+    a.n = n;
+    return a;
+}
+
+size_t cache_ws_bytes(int n) { return fm::align_up((size_t)n * sizeof(int4), 256); }
+
+// ---------------------------------------------------------------- query/key norms and rotation
+fm_status check_rows(const void *p, int64_t ld, int64_t row, int unit, const char *name) {
+    REQUIRE(p && aligned(p, 16), FM_ERR_INVALID_ARG, "%s NULL or not 16-byte aligned", name);
+    REQUIRE(ld >= row && ld % unit == 0, FM_ERR_INVALID_ARG, "%s: ld = %lld (at least %lld, a multiple of 16 bytes)",
+            name, (long long)ld, (long long)row);
+    return FM_OK;
+}
+
+fm_status check_qk(const fm_qk_desc *d, const fm_kv_desc *kv) {
+    REQUIRE(d, FM_ERR_INVALID_ARG, "descriptor is NULL");
+    REQUIRE(d->dtype == FM_F32 || d->dtype == FM_BF16, FM_ERR_UNSUPPORTED, "dtype %d", (int)d->dtype);
+    REQUIRE(d->head_dim == 64 || d->head_dim == 128, FM_ERR_UNSUPPORTED, "head_dim %d (64 or 128)", d->head_dim);
+    REQUIRE(d->T >= 0 && d->T <= (1 << 22), FM_ERR_INVALID_ARG, "T = %d (0 .. 2^22)", d->T);
+    REQUIRE(d->n_heads >= 0 && d->n_kv_heads >= 0 && d->n_heads + d->n_kv_heads >= 1, FM_ERR_INVALID_ARG,
+            "n_heads = %d, n_kv_heads = %d", d->n_heads, d->n_kv_heads);
+    REQUIRE(d->n_heads <= 1024 && d->n_kv_heads <= 1024, FM_ERR_UNSUPPORTED, "n_heads = %d, n_kv_heads = %d (at most 1024)",
+            d->n_heads, d->n_kv_heads);
+    REQUIRE(d->rms_eps >= 0.f && d->rms_eps < INFINITY, FM_ERR_INVALID_ARG, "rms_eps = %g", (double)d->rms_eps);
+    REQUIRE(d->rope_dim >= 0 && d->rope_first >= 0 && d->rope_dim % 2 == 0 && d->rope_first % 2 == 0 &&
+                d->rope_first <= d->head_dim && d->rope_dim <= d->head_dim - d->rope_first,
+            FM_ERR_INVALID_ARG, "rope_dim = %d, rope_first = %d", d->rope_dim, d->rope_first);
+    REQUIRE(d->rope_halves == 0 || d->rope_halves == 1, FM_ERR_INVALID_ARG, "rope_halves = %d", d->rope_halves);
+    REQUIRE(!d->rope_halves || (d->rope_first % 8 == 0 && d->rope_dim % 16 == 0), FM_ERR_UNSUPPORTED,
+            "rope_halves needs rope_first and rope_dim / 2 in multiples of 8");
+    if (d->rope_dim) {
+        REQUIRE(d->rope_base > 1.f && d->rope_base < INFINITY && d->rope_factor >= 1.f && d->rope_factor < INFINITY &&
+                    d->rope_orig_len > 0 && d->beta_slow > 0.f && d->beta_fast > d->beta_slow && d->beta_fast < INFINITY,
+                FM_ERR_INVALID_ARG, "rope_base, rope_factor, rope_orig_len or betas out of range");
+    }
+    if (kv) {
+        CHECK(check_kv_pairs(kv, d->layer));
+        REQUIRE(kv->head_dim == d->head_dim, FM_ERR_INVALID_ARG, "head_dim %d, the cache's is %d", d->head_dim,
+                kv->head_dim);
+        REQUIRE((d->dtype == FM_F32) == (kv->key_dtype == FM_F32), FM_ERR_UNSUPPORTED, "dtype %d with key dtype %d",
+                (int)d->dtype, (int)kv->key_dtype);
+        REQUIRE(d->n_kv_heads >= 1, FM_ERR_INVALID_ARG, "a cache needs n_kv_heads");
+        REQUIRE(d->row_req || d->T == 0 || d->T == kv->B || kv->B == 1, FM_ERR_INVALID_ARG,
+                "row_req NULL needs T == B or B == 1 (T = %d, B = %d)", d->T, kv->B);
+    }
+    if (d->T == 0) return FM_OK;
+    const int unit = d->dtype == FM_F32 ? 4 : 8;
+    const int64_t qrow = (int64_t)d->n_heads * d->head_dim, krow = (int64_t)d->n_kv_heads * d->head_dim;
+    if (d->n_heads) {
+        CHECK(check_rows(d->q, d->q_ld, qrow, unit, "q"));
+        CHECK(check_rows(d->q_out, d->q_out_ld, qrow, unit, "q_out"));
+    }
+    if (d->n_kv_heads) {
+        CHECK(check_rows(d->k, d->k_ld, krow, unit, "k"));
+        REQUIRE(kv || d->k_out, FM_ERR_INVALID_ARG, "k_out NULL without a cache");
+        if (d->k_out) CHECK(check_rows(d->k_out, d->k_out_ld, krow, unit, "k_out"));
+        if (kv) CHECK(check_rows(d->v, d->v_ld, krow, unit, "v"));
+    }
+    REQUIRE((d->q_out != d->q || d->q_out_ld == d->q_ld || !d->n_heads) &&
+                (d->k_out != d->k || d->k_out_ld == d->k_ld || !d->n_kv_heads),
+            FM_ERR_INVALID_ARG, "an output in place needs its input's ld");
+    REQUIRE(aligned(d->q_norm, 16) && aligned(d->k_norm, 16), FM_ERR_INVALID_ARG, "weights not 16-byte aligned");
+    REQUIRE(d->pos, FM_ERR_INVALID_ARG, "pos is NULL");
+    return FM_OK;
 }
 
 // ---------------------------------------------------------------- attention
@@ -602,6 +708,50 @@ fm_status run_attend(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t
 }  // namespace
 
 extern "C" {
+
+fm_status fm_qk_norm_rope(const fm_qk_desc *d, const fm_kv_desc *kv, void *stream) {
+    CHECK(check_qk(d, kv));
+    if (d->T == 0) return ok();
+    fm::QkArgs a;
+    a.q = d->q;
+    a.k = d->k;
+    a.v = d->v;
+    a.q_ld = d->q_ld;
+    a.k_ld = d->k_ld;
+    a.v_ld = d->v_ld;
+    a.q_out = d->q_out;
+    a.k_out = d->k_out;
+    a.q_out_ld = d->q_out_ld;
+    a.k_out_ld = d->k_out_ld;
+    a.q_norm = d->q_norm;
+    a.k_norm = d->k_norm;
+    a.eps = d->rms_eps;
+    a.T = d->T;
+    a.n_heads = d->n_heads;
+    a.n_kv = d->n_kv_heads;
+    a.rope_dim = d->rope_dim;
+    a.rope_first = d->rope_first;
+    a.halves = d->rope_halves;
+    a.pos = d->pos;
+    for (int i = 0; i < fm::kEncMaxPairs; ++i) a.turns[i] = 0.0;
+    if (d->rope_dim) yarn_freqs(d, a.turns);
+    for (int i = 0; i < fm::kEncMaxPairs; ++i) a.turns[i] /= 2.0 * M_PI;
+    a.store = kv != nullptr;
+    a.fp8 = kv && kv->key_dtype == FM_FP8_E4M3_SCALED132;
+    a.k_pool = kv ? const_cast<void *>(kv->pool[2 * d->layer]) : nullptr;
+    a.v_pool = kv ? const_cast<void *>(kv->pool[2 * d->layer + 1]) : nullptr;
+    a.row_req = d->row_req;
+    a.slot = d->slot;
+    a.b_is_zero = kv && !d->row_req && kv->B == 1;
+    a.B = kv ? kv->B : 0;
+    a.bt = kv ? kv->block_table : nullptr;
+    a.bt_ld = kv ? kv->bt_ld : 0;
+    a.seq_lens = kv ? kv->seq_lens : nullptr;
+    a.n_phys = kv ? kv->n_phys_pages : 0;
+    a.max_len = kv ? (int)kv->max_seq_len : 0;
+    CHECK(launched(fm::launch_qk(a, d->dtype == FM_F32, d->head_dim, (hipStream_t)stream), "qk_norm_rope"));
+    return ok();
+}
 
 size_t fm_attend_workspace_bytes(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
     if (check_attend(a, kv, window, n_sink) != FM_OK) return 0;
@@ -851,6 +1001,73 @@ fm_status fm_resident_mask(const fm_query_desc *q_layers, int n_layers, const fm
     c.page_list_ld = page_list_ld;
     c.page_density = page_density;
     CHECK(launched(fm::launch_compact(c, kv->B, st), "page_compact"));
+    return ok();
+}
+
+size_t fm_cache_workspace_bytes(const fm_cache_desc *c, int n) {
+    return check_cache(c, n) == FM_OK ? cache_ws_bytes(n) : 0;
+}
+
+fm_status fm_cache_fork(const fm_cache_desc *c, const int32_t *src, const int32_t *dst, int n, int deep, int32_t *ok_,
+                        void *ws, size_t ws_bytes, void *stream) {
+    CHECK(check_cache(c, n));
+    if (n == 0) return ok();
+    REQUIRE(src && dst, FM_ERR_INVALID_ARG, "src / dst NULL");
+    REQUIRE(ws && aligned(ws, 256) && ws_bytes >= cache_ws_bytes(n), FM_ERR_WORKSPACE,
+            "workspace %zu bytes at %p, need %zu (256-byte aligned)", ws_bytes, ws, cache_ws_bytes(n));
+    fm::CacheArgs a = make_cache(c, n);
+    a.src = src;
+    a.dst = dst;
+    a.deep = deep != 0;
+    a.ok = ok_;
+    a.plan = (int4 *)ws;
+    CHECK(launched(fm::launch_cache_plan(a, true, (hipStream_t)stream), "cache_fork"));
+    return ok();
+}
+
+fm_status fm_cache_grow(const fm_cache_desc *c, const int32_t *req, const int32_t *new_len, int n, int32_t *ok_, void *ws,
+                        size_t ws_bytes, void *stream) {
+    CHECK(check_cache(c, n));
+    if (n == 0) return ok();
+    REQUIRE(req && new_len, FM_ERR_INVALID_ARG, "req / new_len NULL");
+    REQUIRE(ws && aligned(ws, 256) && ws_bytes >= cache_ws_bytes(n), FM_ERR_WORKSPACE,
+            "workspace %zu bytes at %p, need %zu (256-byte aligned)", ws_bytes, ws, cache_ws_bytes(n));
+    fm::CacheArgs a = make_cache(c, n);
+    a.req = req;
+    a.new_len = new_len;
+    a.ok = ok_;
+    a.plan = (int4 *)ws;
+    CHECK(launched(fm::launch_cache_plan(a, false, (hipStream_t)stream), "cache_grow"));
+    return ok();
+}
+
+fm_status fm_cache_free(const fm_cache_desc *c, const int32_t *req, const int32_t *new_len, int n, int32_t *ok_,
+                        void *stream) {
+    CHECK(check_cache(c, n));
+    if (n == 0) return ok();
+    REQUIRE(req, FM_ERR_INVALID_ARG, "req NULL");
+    fm::CacheArgs a = make_cache(c, n);
+    a.req = req;
+    a.new_len = new_len;
+    a.ok = ok_;
+    CHECK(launched(fm::launch_cache_release(a, false, (hipStream_t)stream), "cache_free"));
+    return ok();
+}
+
+fm_status fm_cache_compact(const fm_cache_desc *c, const int32_t *req, const int32_t *start, const int32_t *keep,
+                           int64_t keep_ld, const int32_t *n_keep, int n, int32_t *ok_, void *stream) {
+    CHECK(check_cache(c, n));
+    REQUIRE(keep_ld >= 0 && keep_ld <= INT32_MAX, FM_ERR_INVALID_ARG, "keep_ld = %lld", (long long)keep_ld);
+    if (n == 0) return ok();
+    REQUIRE(req && start && n_keep && (keep || keep_ld == 0), FM_ERR_INVALID_ARG, "req / start / keep / n_keep NULL");
+    fm::CacheArgs a = make_cache(c, n);
+    a.req = req;
+    a.start = start;
+    a.keep = keep;
+    a.keep_ld = keep_ld;
+    a.n_keep = n_keep;
+    a.ok = ok_;
+    CHECK(launched(fm::launch_cache_release(a, true, (hipStream_t)stream), "cache_compact"));
     return ok();
 }
 

@@ -261,6 +261,55 @@ struct AttendArgs {
 int attend_tile_entries(int key_fmt);
 hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s);
 
+// Query/key norms and rotation, keys and values into the pages (qk.hip).
+struct QkArgs {
+    const void *q, *k, *v;    // rows q_ld .. elements apart, heads packed
+    int64_t q_ld, k_ld, v_ld;
+    void *q_out, *k_out;      // k_out nullable
+    int64_t q_out_ld, k_out_ld;
+    const void *q_norm, *k_norm;   // [D] of the input type, or null: that side is not normed
+    float eps;
+    int T, n_heads, n_kv;
+    int rope_dim, rope_first, halves;
+    const int32_t *pos;       // [T]
+    double turns[kEncMaxPairs];    // theta_i / 2 pi
+    // the cache (store != 0)
+    int store, fp8;
+    void *k_pool, *v_pool;
+    const int32_t *row_req, *slot; // [T] or null
+    int b_is_zero, B;
+    const int32_t *bt;
+    int64_t bt_ld;
+    const int32_t *seq_lens;
+    int64_t n_phys;
+    int max_len;
+};
+hipError_t launch_qk(const QkArgs &a, bool f32, int head_dim, hipStream_t s);
+
+// Pages of a cache (cache.hip).
+constexpr int kCacheMaxPages = 1 << 19;       // physical pages (a bitmap in LDS)
+constexpr int kCacheMaxRequests = 1 << 14;    // requests, and entries of a call
+struct CacheArgs {
+    uint8_t *pool[FM_MAX_POOLS];
+    int heads[FM_MAX_POOLS], row_bytes[FM_MAX_POOLS];
+    int n_pools;
+    int32_t *block_table;
+    int64_t bt_ld;
+    int32_t *seq_lens;
+    int B;
+    int32_t *ref, *free_list, *n_free;
+    int64_t n_phys;
+    // the call
+    int n;                       // entries
+    const int32_t *req, *src, *dst, *new_len, *start, *keep, *n_keep;
+    int64_t keep_ld;
+    int deep;
+    int32_t *ok;                 // [n] or null
+    int4 *plan;                  // workspace [n]: forks and growths
+};
+hipError_t launch_cache_release(const CacheArgs &a, bool compact, hipStream_t s);
+hipError_t launch_cache_plan(const CacheArgs &a, bool fork, hipStream_t s);
+
 size_t topk_ws_bytes(int T, int64_t n);   // bytes for T rows of up to n entries (0: not used)
 TopkWs topk_ws_carve(void *ws, int T, int64_t n);
 
