@@ -17,7 +17,7 @@
 // like the rounding of the output itself), their sum is taken before the rounding.
 //
 // Two kernels share that inner step:
-//   attend_split_kernel  few columns (<= 64): the four waves of a workgroup hold the same columns
+//   attend_split_kernel  few columns (<= 32): the four waves of a workgroup hold the same columns
 //                        and each streams tiles of its own, without barriers; bound by memory.
 //   attend_tile_kernel   many columns: a wave has 32 of its own, and the workgroup's four waves
 //                        share each key/value tile; bound by MFMA and the exponentials.
@@ -65,6 +65,13 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 __device__ __forceinline__ f32x16 mma_bf16(const u32x4 &a, const u32x4 &b, const f32x16 &c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// A per-lane value the compiler cannot carry from one tile to the next: what is derived from it (a
+// dozen swizzled LDS addresses) is formed again for every tile, which costs less than holding it.
+__device__ __forceinline__ uint32_t again(uint32_t x) {
+    asm volatile("" : "+v"(x));
+    return x;
 }
 
 template <int N> __device__ __forceinline__ void wait_vm() {     // s_waitcnt vmcnt(N), others left alone
@@ -213,19 +220,37 @@ __device__ __forceinline__ void load_q(QRegs<FMT, D> &q, const AttendArgs &A, in
     }
 }
 
-// S^T of one 32-entry tile.
+// Byte offsets in a tile of the lane's first reads; the others differ by an exclusive or and by
+// whole rows.
 template <int FMT, int D>
-__device__ __forceinline__ f32x16 scores(const uint8_t *kt, int sub, const QRegs<FMT, D> &q) {
+__device__ __forceinline__ uint32_t key_lane() {
     using TL = Tile<FMT, D>;
     const int ln = __lane_id(), h = ln >> 5, r = ln & 31;
-    const uint8_t *row = kt + r * TL::ROW + 32 * sub * TL::ROW;
-    const int sw = TL::swz_k(r);                          // the same 32 rows further on
+    return (uint32_t)(r * TL::ROW + 16 * (h ^ TL::swz_k(r)));
+}
+template <int FMT, int D>
+__device__ __forceinline__ uint32_t value_lane() {
+    using TL = Tile<FMT, D>;
+    const int ln = __lane_id(), h = ln >> 5;
+    if constexpr (TL::F32) {
+        const int j = ln & 31, r = 4 * h;
+        return (uint32_t)(r * TL::ROW + 16 * ((j >> 2) ^ TL::swz_v(r)) + 4 * (j & 3));
+    } else {
+        const int i = ln & 15, g = (ln >> 4) & 1, r = 4 * h + (i >> 2);
+        return (uint32_t)(r * TL::ROW + 16 * ((2 * g + ((i & 3) >> 1)) ^ TL::swz_v(r)) + 8 * (i & 1));
+    }
+}
+
+// S^T of one 32-entry tile; lane: key_lane.
+template <int FMT, int D>
+__device__ __forceinline__ f32x16 scores(const uint8_t *kt, uint32_t lane, int sub, const QRegs<FMT, D> &q) {
+    using TL = Tile<FMT, D>;
     f32x16 s;
 #pragma unroll
     for (int v = 0; v < 16; ++v) s[v] = 0.f;
 #pragma unroll
     for (int i = 0; i < TL::QR; ++i) {
-        const u32x4 a = *(const u32x4 *)(row + 16 * ((2 * i + h) ^ sw));
+        const u32x4 a = *(const u32x4 *)(kt + 32 * sub * TL::ROW + (lane ^ (uint32_t)(32 * i)));
         if constexpr (TL::F32) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -238,34 +263,30 @@ __device__ __forceinline__ f32x16 scores(const uint8_t *kt, int sub, const QRegs
 }
 
 // Column sums over the tile's entries: acc[d, column] += sum_e f(V[e, d]) P[e, column] for the 32
-// values of tile t, f applied to the operand registers.  bf16: P packed, f on pairs; float32: P
-// and f on single values.
+// values of tile t, f applied to the operand registers; lane: value_lane.
 template <int FMT, int D, class F>
-__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, int t, const SRegs<FMT, D> &p,
+__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t, const SRegs<FMT, D> &p,
                                         const PRegs<FMT, D> &pk, f32x16 acc, F f) {
     using TL = Tile<FMT, D>;
-    const int ln = __lane_id(), h = ln >> 5;
     if constexpr (TL::F32) {
-        const int j = ln & 31;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            const int r = 8 * (v >> 2) + 4 * h + (v & 3);
-            const uint32_t x = *(const uint32_t *)(vt + r * TL::ROW + 16 * ((8 * t + (j >> 2)) ^ TL::swz_v(r)) + 4 * (j & 3));
+            const int r = 8 * (v >> 2) + (v & 3);         // and 4 h, in lane
+            const uint32_t at = (lane ^ (uint32_t)(16 * TL::swz_v(r) ^ 128 * t)) + r * TL::ROW;
+            const uint32_t x = *(const uint32_t *)(vt + at);
             acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f(x)), p[0][v], acc, 0, 0, 0);
         }
     } else {
-        const int i = ln & 15, g = (ln >> 4) & 1;
-        const int piece = 4 * t + 2 * g + ((i & 3) >> 1), r = 4 * h + (i >> 2);
-        // rows r, r + 8, ..: one swizzle for all
-        const uint8_t *lane = vt + r * TL::ROW + 16 * (piece ^ TL::swz_v(r)) + 8 * (i & 1);
+        const uint8_t *at = vt + (lane ^ (uint32_t)(64 * t));
 #pragma unroll
         for (int sub = 0; sub < TL::SUB; ++sub)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                const uint8_t *at = lane + (32 * sub + 16 * ks) * TL::ROW;
-                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
+                // rows r, r + 8 of 32 sub + 16 ks ..: one swizzle for all
+                const uint8_t *row = at + (32 * sub + 16 * ks) * TL::ROW;
+                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)row));
                 const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4 *)(at + 8 * TL::ROW)));
+                    (lds_s16x4 *)(row + 8 * TL::ROW)));
                 const u32x4 x = {f(a[0]), f(a[1]), f(b[0]), f(b[1])};
                 acc = mma_bf16(x, pk[sub][ks], acc);
             }
@@ -410,10 +431,12 @@ __device__ __forceinline__ void soften(SRegs<FMT, D> &s, bool masked,
     if (masked) {
         const uint64_t w = vis >> (4 * h);
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub)
+        for (int sub = 0; sub < TL::SUB; ++sub) {
+            const uint32_t half = (uint32_t)(w >> (32 * sub));
 #pragma unroll
             for (int v = 0; v < 16; ++v)
-                s[sub][v] = (w >> (32 * sub + 8 * (v >> 2) + (v & 3))) & 1 ? s[sub][v] : kNegInf;
+                s[sub][v] = half & (1u << (8 * (v >> 2) + (v & 3))) ? s[sub][v] : kNegInf;
+        }
     }
     float mx = s[0][0];
 #pragma unroll
@@ -451,15 +474,14 @@ __device__ __forceinline__ void soften(SRegs<FMT, D> &s, bool masked,
                 for (int b = 0; b < 4; ++b) {
                     const int v = 4 * a + b;
                     const float y = s[sub][v] * k[b];
-                    // a masked entry's scale may be anything
-                    s[sub][v] = masked && !((vis >> (32 * sub + 8 * a + 4 * h + b)) & 1) ? 0.f : y;
+                    s[sub][v] = s[sub][v] == 0.f ? 0.f : y;   // a masked entry's scale may be anything
                 }
             }
     }
 }
 
 template <int FMT, int D>
-__device__ __forceinline__ void add_values(const uint8_t *vt, const SRegs<FMT, D> &p, bool masked,
+__device__ __forceinline__ void add_values(const uint8_t *vt, uint32_t lane, const SRegs<FMT, D> &p, bool masked,
                                            uint64_t vis, State<FMT, D> &st, Special<D> &sp) {
     PRegs<FMT, D> pk;
     pack_p<FMT, D>(p, pk);
@@ -467,12 +489,12 @@ __device__ __forceinline__ void add_values(const uint8_t *vt, const SRegs<FMT, D
         mark_special<FMT, D>(vt, p, vis, sp);
 #pragma unroll
         for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-            st.o[t] = weigh<FMT, D>(vt, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
+            st.o[t] = weigh<FMT, D>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
         return;
     }
 #pragma unroll
     for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-        st.o[t] = weigh<FMT, D>(vt, t, p, pk, st.o[t], [](uint32_t x) { return x; });
+        st.o[t] = weigh<FMT, D>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return x; });
 }
 
 // Copy of a tile from the pool straight into LDS: instruction n of the tile moves 64 pieces.  The
@@ -482,7 +504,7 @@ template <int FMT, int D, bool KEYS>
 __device__ __forceinline__ void copy_pieces(const uint8_t *src, uint8_t *dst, int n) {
     using TL = Tile<FMT, D>;
     constexpr int RI = 1024 / TL::ROW;                    // rows of an instruction
-    const int ln = __lane_id(), r = ln / TL::NP, at = ln % TL::NP;
+    const uint32_t ln = again(__lane_id()), r = ln / TL::NP, at = ln % TL::NP;
     auto swz = [](int r) { return KEYS ? TL::swz_k(r) : TL::swz_v(r); };
     const uint32_t lane = (uint32_t)(r * TL::ROW + 16 * (at ^ swz(r)));
     const uint32_t ofs = lane ^ (uint32_t)(16 * swz(RI * n));   // swz(RI n + r) = swz(RI n) ^ swz(r)
@@ -496,21 +518,19 @@ struct CodeRegs {
     float scale;
 };
 template <int N, int NT>   // N pieces a thread, NT threads
-__device__ __forceinline__ void load_codes(CodeRegs<N> &c, const uint8_t *src, int tid) {
+__device__ __forceinline__ void load_codes(CodeRegs<N> &c, const uint8_t *src, uint32_t tid) {
+    const uint32_t lane = (tid >> 3) * kRowFp8 + 16 * (tid & 7);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int piece = tid + NT * i;
-        c.x[i] = *(const u32x4_u *)(src + (piece >> 3) * kRowFp8 + 16 * (piece & 7));
-    }
+    for (int i = 0; i < N; ++i) c.x[i] = *(const u32x4_u *)(src + lane + (NT / 8) * kRowFp8 * i);
     if (tid < 64) c.scale = *(const float *)(src + tid * kRowFp8 + kDim);
 }
 template <int N, int NT, bool KEYS>
-__device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, int tid) {
+__device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, uint32_t tid) {
     using TL = Tile<KEY_FP8, kDim>;
+    auto swz = [](int r) { return KEYS ? TL::swz_k(r) : TL::swz_v(r); };
+    const uint32_t r = tid >> 3, lane = r * TL::ROW + 16 * ((2 * (tid & 7)) ^ swz(r));
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int piece = tid + NT * i, r = piece >> 3, p = 2 * (piece & 7);
-        const int sw = KEYS ? TL::swz_k(r) : TL::swz_v(r);
+    for (int i = 0; i < N; ++i)
 #pragma unroll
         for (int o = 0; o < 2; ++o) {
             u32x4 y;
@@ -520,16 +540,17 @@ __device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, fl
                 y[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false));
                 y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true));
             }
-            *(u32x4 *)(dst + r * TL::ROW + 16 * ((p + o) ^ sw)) = y;
+            *(u32x4 *)(dst + (lane ^ (uint32_t)(16 * (o ^ swz(NT / 8 * i)))) + NT / 8 * i * TL::ROW) = y;
         }
-    }
     if (tid < 64) scales[tid] = c.scale;
 }
 
 // The page of tile `t` of request b, or -1 where it is not mapped.
 template <int FMT, int D>
 __device__ __forceinline__ int page_of(const AttendArgs &A, int b, int t) {
-    const int page = A.bt[(int64_t)b * A.bt_ld + (int64_t)t * Tile<FMT, D>::E / kPage];
+    // the table is not written meanwhile: a scalar load, which no copy in flight has to be waited for
+    typedef const int32_t __attribute__((address_space(4))) *table;
+    const int page = ((table)(uintptr_t)A.bt)[(int64_t)b * A.bt_ld + (int64_t)t * Tile<FMT, D>::E / kPage];
     return page >= 0 && page < A.n_phys ? page : -1;
 }
 // Where that tile starts in a pool.
@@ -591,20 +612,20 @@ __device__ __forceinline__ void emit(const AttendArgs &A, int R, int row0, int h
 }
 
 // ------------------------------------------------------------------ few columns
-// Workgroup (split, kv head, request): its tiles are dealt to the four waves in turn.  bf16 and
-// float32 tiles are copied straight into the wave's own LDS: the next keys' copy is issued once
-// the scores are formed and the next values' once they are weighed, so each wave has one to two
-// copies in flight and waits for no other wave.  fp8 tiles are loaded a tile ahead into
-// registers.  NB: blocks of 32 columns a wave holds.
-template <int FMT, int D, int NB>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(FMT == KEY_FP8 && NB == 1 ? 2 : 1)))
+// Workgroup (split, kv head, request), at most 32 columns: its tiles are dealt to the four waves
+// in turn.  bf16 and float32 tiles are copied straight into the wave's own LDS: the next keys' copy
+// is issued once the scores are formed and the next values' once they are weighed, so each wave
+// has one to two copies in flight and waits for no other wave.  fp8 tiles are loaded a tile ahead
+// into registers.
+template <int FMT, int D>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1)))
 void attend_split_kernel(AttendArgs A) {
     using TL = Tile<FMT, D>;
     constexpr bool FP8 = FMT == KEY_FP8;
     constexpr int NI = TL::BYTES / 1024;
     __shared__ __align__(16) uint8_t sK[4][TL::BYTES], sV[FP8 ? 1 : 4][FP8 ? 16 : TL::BYTES];
     __shared__ float sS[FP8 ? 4 : 1][2][64], sM[4][32], sL[4][32];
-    __shared__ Special<D> sX[4][NB];
+    __shared__ Special<D> sX[4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
     const int split = blockIdx.x % A.splits, hk = (blockIdx.x / A.splits) % A.n_kv, b = blockIdx.x / (A.splits * A.n_kv);
     const Req rq = request(A, b);
@@ -613,18 +634,14 @@ void attend_split_kernel(AttendArgs A) {
     const Span sp = make_span<TL::E>(A, 0, rq.n - 1, rq.n, rq.len);
     const int per = (sp.count + A.splits - 1) / A.splits;
     const int t0 = split * per + w, t1 = min(sp.count, (split + 1) * per);
-    Col col[NB];
-    u32x4 q[NB][TL::QR];
-    State<FMT, D> st[NB];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        const int R = 32 * n + j;
-        col[n] = make_col(A, R, rq.row0, rq.n, rq.len);
-        load_q<FMT, D>(q[n], A, R, rq.row0, hk, col[n].valid);
-        st[n].clear();
-        clear_special(sX[w][n]);
-    }
+    const Col col = make_col(A, j, rq.row0, rq.n, rq.len);
+    u32x4 q[TL::QR];
+    State<FMT, D> st;
+    load_q<FMT, D>(q, A, j, rq.row0, hk, col.valid);
+    st.clear();
+    clear_special(sX[w]);
     const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
+    const uint32_t key0 = key_lane<FMT, D>(), value0 = value_lane<FMT, D>();
     uint8_t *kt = sK[w], *vt = FP8 ? sK[w] : sV[FP8 ? 0 : w];
     // the next mapped tile from i on, and its page (i >= t1: none)
     int page = -1;
@@ -639,15 +656,15 @@ void attend_split_kernel(AttendArgs A) {
     CodeRegs<FP8 ? 8 : 1> kc, vc;
     auto issue_k = [&](int t) {
         const uint8_t *src = kp + tile_at<FMT, D>(A, page, hk, t);
-        if constexpr (FP8) load_codes<8, 64>(kc, src, ln);
+        if constexpr (FP8) load_codes<8, 64>(kc, src, again(ln));
         else {
 #pragma unroll
             for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(src, kt, n);
         }
     };
-    auto issue_v = [&](int t, int pg) {
-        const uint8_t *src = vp + tile_at<FMT, D>(A, pg, hk, t);
-        if constexpr (FP8) load_codes<8, 64>(vc, src, ln);
+    auto issue_v = [&](int t) {
+        const uint8_t *src = vp + tile_at<FMT, D>(A, page, hk, t);
+        if constexpr (FP8) load_codes<8, 64>(vc, src, again(ln));
         else {
 #pragma unroll
             for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(src, vt, n);
@@ -656,82 +673,71 @@ void attend_split_kernel(AttendArgs A) {
     int i = seek(t0);
     if (i < t1) {
         issue_k(sp.at(i));
-        issue_v(sp.at(i), page);
+        issue_v(sp.at(i));
     }
     while (i < t1) {
         const int t = sp.at(i), s0 = t * TL::E;
         const int nx = seek(i + 4);
+        const uint32_t me = again(ln), klane = again(key0), vlane = again(value0);
         if constexpr (FP8) {
-            put_codes<8, 64, true>(kc, kt, sS[w][0], ln);
+            put_codes<8, 64, true>(kc, kt, sS[w][0], me);
             __builtin_amdgcn_wave_barrier();
         } else {
             wait_vm<NI>();                                // the keys; the values may be in flight
         }
-        f32x16 s[NB][TL::SUB];
+        f32x16 s[TL::SUB];
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub)
-#pragma unroll
-            for (int n = 0; n < NB; ++n) s[n][sub] = scores<FMT, D>(kt, sub, q[n]);
+        for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, klane, sub, q);
         __builtin_amdgcn_s_waitcnt(0xc07f);               // lgkmcnt(0): the keys are read
         __builtin_amdgcn_sched_barrier(0);
         if (nx < t1) issue_k(sp.at(nx));
         if constexpr (FP8) {
-            put_codes<8, 64, false>(vc, vt, sS[w][1], ln);
+            put_codes<8, 64, false>(vc, vt, sS[w][1], me);
             __builtin_amdgcn_wave_barrier();
-            if (nx < t1) issue_v(sp.at(nx), page);
+            if (nx < t1) issue_v(sp.at(nx));
         }
-        uint64_t vis[NB];
-        bool masked[NB];
         constexpr uint64_t full = ~0ull >> (64 - TL::E);
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            vis[n] = col[n].valid ? visible(col[n], s0, A.mask_ld) & full : full;
-            masked[n] = __ballot(vis[n] != full) != 0;
-            soften<FMT, D>(s[n], masked[n], vis[n], A.c, sS[FP8 ? w : 0][0], sS[FP8 ? w : 0][1], st[n]);
-        }
+        const uint64_t vis = col.valid ? visible(col, s0, A.mask_ld) & full : full;
+        const bool masked = __ballot(vis != full) != 0;
+        soften<FMT, D>(s, masked, vis, A.c, sS[FP8 ? w : 0][0], sS[FP8 ? w : 0][1], st);
         if constexpr (!FP8) {
             if (nx < t1) wait_vm<NI>();                   // the values; the next keys may be in flight
             else wait_vm<0>();
         }
-#pragma unroll
-        for (int n = 0; n < NB; ++n) add_values<FMT, D>(vt, s[n], masked[n], vis[n], st[n], sX[w][n]);
+        add_values<FMT, D>(vt, vlane, s, masked, vis, st, sX[w]);
         __builtin_amdgcn_s_waitcnt(0xc07f);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (!FP8) {
-            if (nx < t1) issue_v(sp.at(nx), page);
+            if (nx < t1) issue_v(sp.at(nx));
         }
         i = nx;
     }
-    // the four waves' parts of each block of columns, joined and written by all threads
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-        if (n) __syncthreads();
-        const float l = st[n].l + other_half(st[n].l);
-        if (ln < 32) {
-            sM[w][j] = st[n].m;
-            sL[w][j] = l;
-        }
-        apply_special<FMT, D>(sX[w][n], st[n]);
-        stage_o<FMT, D>(kt, st[n]);
-        __syncthreads();
+    // the four waves' parts, joined and written by all threads
+    const float l = st.l + other_half(st.l);
+    if (ln < 32) {
+        sM[w][j] = st.m;
+        sL[w][j] = l;
+    }
+    apply_special<FMT, D>(sX[w], st);
+    stage_o<FMT, D>(kt, st);
+    __syncthreads();
 #pragma unroll 1
-        for (int e = tid; e < 32 * (D / 4); e += 256) {
-            const int c = e / (D / 4), piece = e % (D / 4), R = 32 * n + c;
-            if (R >= cols) continue;
-            float m = kNegInf, sum = 0.f;
+    for (int e = tid; e < 32 * (D / 4); e += 256) {
+        const int c = e / (D / 4), piece = e % (D / 4);
+        if (c >= cols) continue;
+        float m = kNegInf, sum = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m = fmaxf(m, sM[k][c]);
-            f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, sM[k][c]);
+        f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float mk = sM[k][c];
-                const float f = mk == kNegInf ? 0.f : __builtin_amdgcn_exp2f((mk - m) * A.c);
-                if (sL[k][c] == 0.f) continue;            // nothing seen
-                sum += f * sL[k][c];
-                o += f * *stage_at<D>(sK[k], c, piece);
-            }
-            emit<FMT, D>(A, R, rq.row0, hk, split, piece, o, m, sum);
+        for (int k = 0; k < 4; ++k) {
+            const float mk = sM[k][c];
+            const float f = mk == kNegInf ? 0.f : __builtin_amdgcn_exp2f((mk - m) * A.c);
+            if (sL[k][c] == 0.f) continue;                // nothing seen
+            sum += f * sL[k][c];
+            o += f * *stage_at<D>(sK[k], c, piece);
         }
+        emit<FMT, D>(A, c, rq.row0, hk, split, piece, o, m, sum);
     }
 }
 
@@ -769,6 +775,7 @@ void attend_tile_kernel(AttendArgs A) {
     State<FMT, D> st;
     st.clear();
     clear_special(sX[w]);
+    const uint32_t key0 = key_lane<FMT, D>(), value0 = value_lane<FMT, D>();
     const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
     int page = -1;
     auto seek = [&](int i) {
@@ -783,8 +790,8 @@ void attend_tile_kernel(AttendArgs A) {
     auto issue = [&](uint8_t *kt, uint8_t *vt, int t) {
         const int64_t at = tile_at<FMT, D>(A, page, hk, t);
         if constexpr (FP8) {
-            load_codes<2, 256>(kc, kp + at, tid);
-            load_codes<2, 256>(vc, vp + at, tid);
+            load_codes<2, 256>(kc, kp + at, again(tid));
+            load_codes<2, 256>(vc, vp + at, again(tid));
         } else {
 #pragma unroll
             for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + at, kt, NI * w + n);
@@ -798,18 +805,20 @@ void attend_tile_kernel(AttendArgs A) {
         if (idle || __ballot(col.valid && vis != 0) == 0) return;
         const bool masked = __ballot(vis != full) != 0;
         f32x16 s[TL::SUB];
+        const uint32_t klane = again(key0);
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, sub, q);
+        for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, klane, sub, q);
         soften<FMT, D>(s, masked, vis, A.c, ks, vs, st);
-        add_values<FMT, D>(vt, s, masked, vis, st, sX[w]);
+        add_values<FMT, D>(vt, again(value0), s, masked, vis, st, sX[w]);
     };
     int i = seek(t0);
     // tile i is on its way to (kt, vt); after the barrier the other stage is free for the next
     auto step = [&](uint8_t *kt, uint8_t *vt, uint8_t *kn, uint8_t *vn, int stage) {
         const int t = sp.at(i);
         if constexpr (FP8) {
-            put_codes<2, 256, true>(kc, kt, sS[stage][0], tid);
-            put_codes<2, 256, false>(vc, vt, sS[stage][1], tid);
+            const uint32_t me = again(tid);
+            put_codes<2, 256, true>(kc, kt, sS[stage][0], me);
+            put_codes<2, 256, false>(vc, vt, sS[stage][1], me);
         } else {
             wait_vm<0>();
         }
@@ -883,8 +892,7 @@ hipError_t launch(const AttendArgs &a, hipStream_t s) {
         attend_tile_kernel<FMT, D><<<dim3((unsigned)(a.splits * a.blocks * a.n_kv * a.B)), 256, 0, s>>>(a);
     } else {
         const dim3 grid((unsigned)(a.splits * a.n_kv * a.B));
-        if (a.max_rows * a.G <= 32) attend_split_kernel<FMT, D, 1><<<grid, 256, 0, s>>>(a);
-        else attend_split_kernel<FMT, D, 2><<<grid, 256, 0, s>>>(a);
+        attend_split_kernel<FMT, D><<<grid, 256, 0, s>>>(a);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;

@@ -629,7 +629,7 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     return FM_OK;
 }
 
-// The kernel and the split of the entries: up to 64 columns (rows x heads of a kv head) take the
+// The kernel and the split of the entries: up to 32 columns (rows x heads of a kv head) take the
 // kernel whose waves stream tiles of their own, more take 128-column blocks.  Entries are split
 // over more workgroups while there are fewer than kAttendTarget and each keeps kAttendMinTiles.
 #ifndef FM_ATTEND_TARGET
@@ -647,8 +647,8 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     if (a->T == 0 || a->max_rows == 0) return p;
     const int G = a->n_heads / a->n_kv_heads;
     const int64_t cols = (int64_t)a->max_rows * G;
-    p.blocks = cols <= 64 ? 0 : (int)((cols + 127) / 128);
-    const int64_t rows = std::min<int64_t>(a->max_rows, (p.blocks ? 128 : 64) / G + 2);
+    p.blocks = cols <= 32 ? 0 : (int)((cols + 127) / 128);
+    const int64_t rows = std::min<int64_t>(a->max_rows, (p.blocks ? 128 : 32) / G + 2);
     const int E = fm::attend_tile_entries(key_fmt(kv->key_dtype));
     const int64_t seen = std::min<int64_t>(std::min<int64_t>(window, kv->max_seq_len) + rows +
                                                std::min<int64_t>(n_sink, kv->max_seq_len), kv->max_seq_len);
