@@ -27,6 +27,7 @@
 // the test.  A masked entry's key can hold anything (its score is replaced), and so can its
 // value: 0 * inf would reach the sum through the product, so tiles with masked entries are
 // searched for values that are not finite, and what those do is kept apart (Special, below).
+#include <algorithm>
 #include <type_traits>
 
 #include "fm_internal.h"
@@ -52,9 +53,21 @@ constexpr float kNegInf = -__builtin_inff();
 // until then the exponentials stay below 2^8, far from overflow, and the sums need no rescaling.
 constexpr float kLazy = 8.f;
 
-__device__ __forceinline__ float other_half(float x) {     // the value of lane ^ 32
-    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return __uint_as_float(__lane_id() < 32 ? s[1] : s[0]);
+// The two halves' values of a column (of lane j and lane j + 32), in both lanes.
+struct Halves {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Halves halves(uint32_t x) {
+    const auto s = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return {s[0], s[1]};
+}
+__device__ __forceinline__ float both_max(float x) {
+    const Halves y = halves(__float_as_uint(x));
+    return fmaxf(__uint_as_float(y.lo), __uint_as_float(y.hi));
+}
+__device__ __forceinline__ float both_sum(float x) {
+    const Halves y = halves(__float_as_uint(x));
+    return __uint_as_float(y.lo) + __uint_as_float(y.hi);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -108,8 +121,9 @@ struct Tile {
 };
 
 template <int FMT, int D> using QRegs = u32x4[Tile<FMT, D>::QR];
-template <int FMT, int D> using PRegs = u32x4[Tile<FMT, D>::SUB][2];
-template <int FMT, int D> using SRegs = f32x16[Tile<FMT, D>::SUB];
+// Scores (then probabilities) of NS 32-entry tiles, and their packed form.
+template <int NS> using SRegs = f32x16[NS];
+template <int NS> using PRegs = u32x4[NS][2];
 
 // One problem's columns: position, limits and masks of the lane's row.
 struct Col {
@@ -195,13 +209,14 @@ template <int FMT, int D>
 struct State {
     f32x16 o[Tile<FMT, D>::DT];
     float m, l;       // m: maximum in score units (both halves alike), l: the lane's own entries
+    float mc;         // m times c, 0 while nothing was seen
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int t = 0; t < Tile<FMT, D>::DT; ++t)
 #pragma unroll
             for (int v = 0; v < 16; ++v) o[t][v] = 0.f;
         m = kNegInf;
-        l = 0.f;
+        l = mc = 0.f;
     }
 };
 
@@ -262,11 +277,11 @@ __device__ __forceinline__ f32x16 scores(const uint8_t *kt, uint32_t lane, int s
     return s;
 }
 
-// Column sums over the tile's entries: acc[d, column] += sum_e f(V[e, d]) P[e, column] for the 32
-// values of tile t, f applied to the operand registers; lane: value_lane.
-template <int FMT, int D, class F>
-__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t, const SRegs<FMT, D> &p,
-                                        const PRegs<FMT, D> &pk, f32x16 acc, F f) {
+// Column sums over the entries of NS 32-entry tiles: acc[d, column] += sum_e f(V[e, d]) P[e, column]
+// for the 32 values of tile t, f applied to the operand registers; lane: value_lane.
+template <int FMT, int D, int NS, class F>
+__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t, const SRegs<NS> &p,
+                                        const PRegs<NS> &pk, f32x16 acc, F f) {
     using TL = Tile<FMT, D>;
     if constexpr (TL::F32) {
 #pragma unroll
@@ -279,7 +294,7 @@ __device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t,
     } else {
         const uint8_t *at = vt + (lane ^ (uint32_t)(64 * t));
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub)
+        for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 // rows r, r + 8 of 32 sub + 16 ks ..: one swizzle for all
@@ -294,11 +309,11 @@ __device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t,
     return acc;
 }
 
-template <int FMT, int D>
-__device__ __forceinline__ void pack_p(const SRegs<FMT, D> &p, PRegs<FMT, D> &pk) {
+template <int FMT, int NS>
+__device__ __forceinline__ void pack_p(const SRegs<NS> &p, PRegs<NS> &pk) {
     if constexpr (FMT != KEY_F32) {
 #pragma unroll
-        for (int sub = 0; sub < Tile<FMT, D>::SUB; ++sub)
+        for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
@@ -322,23 +337,21 @@ __device__ __forceinline__ void clear_special(Special<D> &sp) {
     for (int i = __lane_id(); i < (int)(sizeof(Special<D>) / 4); i += 64) x[i] = 0;
 }
 
-// Marks what the tile's infinities and NaNs do to the columns that see them.  Rolled loops over
-// the tile in LDS: such tiles are rare, and the wave's registers stay where they are.
-template <int FMT, int D>
-__device__ __forceinline__ void mark_special(const uint8_t *vt, const SRegs<FMT, D> &p, uint64_t vis,
-                                             Special<D> &sp) {
+// Marks what the infinities and NaNs of NS 32-entry tiles (at vt) do to the columns that see them;
+// vis: bit e for entry e.  Rolled loops over LDS: such tiles are rare, and the wave's registers
+// stay where they are.
+template <int FMT, int D, int NS>
+__device__ __forceinline__ void mark_special(const uint8_t *vt, const SRegs<NS> &p, uint64_t vis, Special<D> &sp) {
     using TL = Tile<FMT, D>;
     const int ln = __lane_id(), h = ln >> 5;
-    uint32_t dead[2] = {0u, 0u};
 #pragma unroll
-    for (int sub = 0; sub < TL::SUB; ++sub)
+    for (int i = 0; i < NS; ++i) {
+        uint32_t own = 0;
 #pragma unroll
-        for (int v = 0; v < 16; ++v)
-            dead[sub] |= p[sub][v] == 0.f ? 1u << (8 * (v >> 2) + (v & 3)) : 0u;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t own = dead[i] << (4 * h);
-        const uint32_t both = own | __float_as_uint(other_half(__uint_as_float(own)));
+        for (int v = 0; v < 16; ++v) own |= p[i][v] == 0.f ? 1u << (8 * (v >> 2) + (v & 3)) : 0u;
+        own <<= 4 * h;
+        const Halves y = halves(own);
+        const uint32_t both = y.lo | y.hi;
         if (ln < 32) {
             sp.vis[ln][i] = (uint32_t)(vis >> (32 * i));
             sp.dead[ln][i] = both;
@@ -348,7 +361,7 @@ __device__ __forceinline__ void mark_special(const uint8_t *vt, const SRegs<FMT,
     __builtin_amdgcn_wave_barrier();
     constexpr int W = TL::F32 ? 1 : 2;                     // values of a dword
 #pragma unroll 1
-    for (int x = ln; x < TL::BYTES / 4; x += 64) {
+    for (int x = ln; x < NS * 32 * TL::ROW / 4; x += 64) {
         const int r = x / (TL::ROW / 4), at = x % (TL::ROW / 4);
         const int d0 = (4 * ((at >> 2) ^ TL::swz_v(r)) + (at & 3)) * W;
         const uint32_t word = *(const uint32_t *)(vt + 4 * x);
@@ -411,62 +424,77 @@ __device__ __forceinline__ bool any_special(const uint8_t *vt) {
     return __ballot((bad & 0x80008000u) != 0) != 0;
 }
 
-// The softmax step of a tile for one column: the scores become exponentials, the state is rescaled.
-// c: scale * log2 e.  ks, vs: the entries' fp8 scales of the tile (null otherwise).
-template <int FMT, int D>
-__device__ __forceinline__ void soften(SRegs<FMT, D> &s, bool masked,
-                                       uint64_t vis, float c, const float *ks, const float *vs, State<FMT, D> &st) {
-    using TL = Tile<FMT, D>;
+// fp8: scores times their entries' key scales.
+template <int NS>
+__device__ __forceinline__ void scale_scores(SRegs<NS> &s, const float *ks) {
     const int h = __lane_id() >> 5;
-    if constexpr (FMT == KEY_FP8) {
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub)
+    for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                const f32x4 k = *(const f32x4 *)(ks + 32 * sub + 8 * a + 4 * h);
+        for (int a = 0; a < 4; ++a) {
+            const f32x4 k = *(const f32x4 *)(ks + 32 * sub + 8 * a + 4 * h);
 #pragma unroll
-                for (int b = 0; b < 4; ++b) s[sub][4 * a + b] *= k[b];
-            }
-    }
-    if (masked) {
-        const uint64_t w = vis >> (4 * h);
-#pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub) {
-            const uint32_t half = (uint32_t)(w >> (32 * sub));
-#pragma unroll
-            for (int v = 0; v < 16; ++v)
-                s[sub][v] = half & (1u << (8 * (v >> 2) + (v & 3))) ? s[sub][v] : kNegInf;
+            for (int b = 0; b < 4; ++b) s[sub][4 * a + b] *= k[b];
         }
+}
+
+// Scores of the entries whose bit in vis is clear become -inf.
+template <int NS>
+__device__ __forceinline__ void hide(SRegs<NS> &s, uint64_t vis) {
+    const uint64_t w = vis >> (4 * (__lane_id() >> 5));
+#pragma unroll
+    for (int sub = 0; sub < NS; ++sub) {
+        const uint32_t half = (uint32_t)(w >> (32 * sub));
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[sub][v] = half & (1u << (8 * (v >> 2) + (v & 3))) ? s[sub][v] : kNegInf;
     }
+}
+
+template <int NS>
+__device__ __forceinline__ float max_of(const SRegs<NS> &s) {
     float mx = s[0][0];
 #pragma unroll
-    for (int sub = 0; sub < TL::SUB; ++sub)
+    for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
         for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[sub][v]);
-    mx = fmaxf(mx, other_half(mx));
-    if (__ballot((mx - st.m) * c > kLazy || (st.m == kNegInf && mx > kNegInf))) {
+    return mx;
+}
+
+// The column's maximum, raised (and the sums with it) where mx, the lane's new scores', calls for it.
+template <int FMT, int D>
+__device__ __forceinline__ void raise_max(float mx, float c, State<FMT, D> &st) {
+    mx = both_max(mx);
+    // where nothing was seen yet, m is -inf and any score exceeds it by inf
+    if (__builtin_amdgcn_ballot_w64((mx - st.m) * c > kLazy)) {
         const float m = fmaxf(st.m, mx);
         const float a = st.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((st.m - m) * c);
         st.m = m;
+        st.mc = m == kNegInf ? 0.f : m * c;
         st.l *= a;
 #pragma unroll
-        for (int t = 0; t < TL::DT; ++t)
+        for (int t = 0; t < Tile<FMT, D>::DT; ++t)
 #pragma unroll
             for (int v = 0; v < 16; ++v) st.o[t][v] *= a;
     }
-    const float mc = st.m == kNegInf ? 0.f : st.m * c;
-    float sum = 0.f;
+}
+
+// Scores to exponentials, their sum to l, and (fp8; vs: the entries' value scales) scaled for the
+// product with the codes.  c: scale * log2 e.
+template <int FMT, int D, int NS>
+__device__ __forceinline__ void exponentials(SRegs<NS> &s, bool masked, float c, const float *vs, State<FMT, D> &st) {
+    const int h = __lane_id() >> 5;
+    float sum[2] = {st.l, 0.f};
 #pragma unroll
-    for (int sub = 0; sub < TL::SUB; ++sub)
+    for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            s[sub][v] = __builtin_amdgcn_exp2f(fmaf(s[sub][v], c, -mc));
-            sum += s[sub][v];
+            s[sub][v] = __builtin_amdgcn_exp2f(fmaf(s[sub][v], c, -st.mc));
+            sum[v & 1] += s[sub][v];
         }
-    st.l += sum;
+    st.l = sum[0] + sum[1];
     if constexpr (FMT == KEY_FP8) {
 #pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub)
+        for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
                 const f32x4 k = *(const f32x4 *)(vs + 32 * sub + 8 * a + 4 * h);
@@ -474,27 +502,37 @@ __device__ __forceinline__ void soften(SRegs<FMT, D> &s, bool masked,
                 for (int b = 0; b < 4; ++b) {
                     const int v = 4 * a + b;
                     const float y = s[sub][v] * k[b];
-                    s[sub][v] = s[sub][v] == 0.f ? 0.f : y;   // a masked entry's scale may be anything
+                    s[sub][v] = masked && s[sub][v] == 0.f ? 0.f : y;   // a masked entry's scale may be anything
                 }
             }
     }
 }
 
-template <int FMT, int D>
-__device__ __forceinline__ void add_values(const uint8_t *vt, uint32_t lane, const SRegs<FMT, D> &p, bool masked,
+template <int FMT, int D, int NS>
+__device__ __forceinline__ void soften(SRegs<NS> &s, bool masked, uint64_t vis, float c, const float *ks, const float *vs,
+                                       State<FMT, D> &st) {
+    if constexpr (FMT == KEY_FP8) scale_scores<NS>(s, ks);
+    if (masked) hide<NS>(s, vis);
+    raise_max<FMT, D>(max_of<NS>(s), c, st);
+    exponentials<FMT, D, NS>(s, masked, c, vs, st);
+}
+
+// The values of NS 32-entry tiles at vt; special: some are not finite and some entries are masked.
+template <int FMT, int D, int NS>
+__device__ __forceinline__ void add_values(const uint8_t *vt, uint32_t lane, const SRegs<NS> &p, bool special,
                                            uint64_t vis, State<FMT, D> &st, Special<D> &sp) {
-    PRegs<FMT, D> pk;
-    pack_p<FMT, D>(p, pk);
-    if (masked && any_special<FMT, D>(vt)) {
-        mark_special<FMT, D>(vt, p, vis, sp);
+    PRegs<NS> pk;
+    pack_p<FMT, NS>(p, pk);
+    if (special) {
+        mark_special<FMT, D, NS>(vt, p, vis, sp);
 #pragma unroll
         for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-            st.o[t] = weigh<FMT, D>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
+            st.o[t] = weigh<FMT, D, NS>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
         return;
     }
 #pragma unroll
     for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-        st.o[t] = weigh<FMT, D>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return x; });
+        st.o[t] = weigh<FMT, D, NS>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return x; });
 }
 
 // Copy of a tile from the pool straight into LDS: instruction n of the tile moves 64 pieces.  The
@@ -511,6 +549,8 @@ __device__ __forceinline__ void copy_pieces(const uint8_t *src, uint8_t *dst, in
     __builtin_amdgcn_global_load_lds((const void *)(src + 1024 * n + ofs), (lds_void *)(dst + 1024 * n), 16, 0, 0);
 }
 
+constexpr auto as_is = [](int, int, u32x4 y) { return y; };   // a piece as it was loaded
+
 // fp8 tiles pass through registers: 16 codes a piece, widened exactly to bf16.
 template <int N>
 struct CodeRegs {
@@ -524,8 +564,8 @@ __device__ __forceinline__ void load_codes(CodeRegs<N> &c, const uint8_t *src, u
     for (int i = 0; i < N; ++i) c.x[i] = *(const u32x4_u *)(src + lane + (NT / 8) * kRowFp8 * i);
     if (tid < 64) c.scale = *(const float *)(src + tid * kRowFp8 + kDim);
 }
-template <int N, int NT, bool KEYS>
-__device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, uint32_t tid) {
+template <int N, int NT, bool KEYS, class F>
+__device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, uint32_t tid, F fix) {
     using TL = Tile<KEY_FP8, kDim>;
     auto swz = [](int r) { return KEYS ? TL::swz_k(r) : TL::swz_v(r); };
     const uint32_t r = tid >> 3, lane = r * TL::ROW + 16 * ((2 * (tid & 7)) ^ swz(r));
@@ -540,7 +580,8 @@ __device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, fl
                 y[2 * w] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, false));
                 y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true));
             }
-            *(u32x4 *)(dst + (lane ^ (uint32_t)(16 * (o ^ swz(NT / 8 * i)))) + NT / 8 * i * TL::ROW) = y;
+            *(u32x4 *)(dst + (lane ^ (uint32_t)(16 * (o ^ swz(NT / 8 * i)))) + NT / 8 * i * TL::ROW) =
+                fix(r + NT / 8 * i, 2 * (tid & 7) + o, y);
         }
     if (tid < 64) scales[tid] = c.scale;
 }
@@ -680,7 +721,7 @@ void attend_split_kernel(AttendArgs A) {
         const int nx = seek(i + 4);
         const uint32_t me = again(ln), klane = again(key0), vlane = again(value0);
         if constexpr (FP8) {
-            put_codes<8, 64, true>(kc, kt, sS[w][0], me);
+            put_codes<8, 64, true>(kc, kt, sS[w][0], me, as_is);
             __builtin_amdgcn_wave_barrier();
         } else {
             wait_vm<NI>();                                // the keys; the values may be in flight
@@ -692,19 +733,19 @@ void attend_split_kernel(AttendArgs A) {
         __builtin_amdgcn_sched_barrier(0);
         if (nx < t1) issue_k(sp.at(nx));
         if constexpr (FP8) {
-            put_codes<8, 64, false>(vc, vt, sS[w][1], me);
+            put_codes<8, 64, false>(vc, vt, sS[w][1], me, as_is);
             __builtin_amdgcn_wave_barrier();
             if (nx < t1) issue_v(sp.at(nx));
         }
         constexpr uint64_t full = ~0ull >> (64 - TL::E);
         const uint64_t vis = col.valid ? visible(col, s0, A.mask_ld) & full : full;
         const bool masked = __ballot(vis != full) != 0;
-        soften<FMT, D>(s, masked, vis, A.c, sS[FP8 ? w : 0][0], sS[FP8 ? w : 0][1], st);
+        soften<FMT, D, TL::SUB>(s, masked, vis, A.c, sS[FP8 ? w : 0][0], sS[FP8 ? w : 0][1], st);
         if constexpr (!FP8) {
             if (nx < t1) wait_vm<NI>();                   // the values; the next keys may be in flight
             else wait_vm<0>();
         }
-        add_values<FMT, D>(vt, vlane, s, masked, vis, st, sX[w]);
+        add_values<FMT, D, TL::SUB>(vt, vlane, s, masked && any_special<FMT, D>(vt), vis, st, sX[w]);
         __builtin_amdgcn_s_waitcnt(0xc07f);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (!FP8) {
@@ -713,7 +754,7 @@ void attend_split_kernel(AttendArgs A) {
         i = nx;
     }
     // the four waves' parts, joined and written by all threads
-    const float l = st.l + other_half(st.l);
+    const float l = both_sum(st.l);
     if (ln < 32) {
         sM[w][j] = st.m;
         sL[w][j] = l;
@@ -808,8 +849,8 @@ void attend_tile_kernel(AttendArgs A) {
         const uint32_t klane = again(key0);
 #pragma unroll
         for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, klane, sub, q);
-        soften<FMT, D>(s, masked, vis, A.c, ks, vs, st);
-        add_values<FMT, D>(vt, again(value0), s, masked, vis, st, sX[w]);
+        soften<FMT, D, TL::SUB>(s, masked, vis, A.c, ks, vs, st);
+        add_values<FMT, D, TL::SUB>(vt, again(value0), s, masked && any_special<FMT, D>(vt), vis, st, sX[w]);
     };
     int i = seek(t0);
     // tile i is on its way to (kt, vt); after the barrier the other stage is free for the next
@@ -817,8 +858,8 @@ void attend_tile_kernel(AttendArgs A) {
         const int t = sp.at(i);
         if constexpr (FP8) {
             const uint32_t me = again(tid);
-            put_codes<2, 256, true>(kc, kt, sS[stage][0], me);
-            put_codes<2, 256, false>(vc, vt, sS[stage][1], me);
+            put_codes<2, 256, true>(kc, kt, sS[stage][0], me, as_is);
+            put_codes<2, 256, false>(vc, vt, sS[stage][1], me, as_is);
         } else {
             wait_vm<0>();
         }
@@ -835,7 +876,7 @@ void attend_tile_kernel(AttendArgs A) {
     }
     __syncthreads();
     uint8_t *stage = w == 0 ? sK0 : w == 1 ? sV0 : w == 2 ? sK1 : sV1;
-    const float l = st.l + other_half(st.l);
+    const float l = both_sum(st.l);
     apply_special<FMT, D>(sX[w], st);
     stage_o<FMT, D>(stage, st);
     __builtin_amdgcn_wave_barrier();
@@ -845,6 +886,317 @@ void attend_tile_kernel(AttendArgs A) {
         const float mc = __shfl(st.m, c), lc = __shfl(l, c);
         if (c0 + 32 * w + c < cols)
             emit<FMT, D>(A, c0 + 32 * w + c, rq.row0, hk, split, piece, *stage_at<D>(stage, c, piece), mc, lc);
+    }
+}
+
+// ------------------------------------------------------------------ many columns, long runs
+// Workgroup (split, block of 256 columns, kv head, request) of eight waves, bf16 and fp8 caches.
+// Each wave keeps the matrix unit busy with its own instructions: while a 32-entry tile's
+// exponentials are formed, the next tile's scores run, and while its values are weighed, the next
+// scores' mask and maximum.  Tiles pass through registers (loaded a tile ahead) into three LDS
+// stages, with one barrier a 64-entry tile: when all waves have met in tile i, tile i + 1 is
+// there and the stage of tile i - 1 is free.
+constexpr int kLongNT = 512;
+template <int FMT, int D>
+struct Staged {
+    using TL = Tile<FMT, D>;
+    static constexpr int N = TL::BYTES / (16 * kLongNT);   // 16-byte pieces a thread
+    u32x4 k[N], v[N];
+    __device__ __forceinline__ void load(const uint8_t *kp, const uint8_t *vp, int tid) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) k[n] = *(const u32x4 *)(kp + 16 * kLongNT * n + 16u * (uint32_t)tid);
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = *(const u32x4 *)(vp + 16 * kLongNT * n + 16u * (uint32_t)tid);
+    }
+    // fix(row, piece, values): what is written of a piece of values
+    template <class F>
+    __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, float *, float *, int tid, F fix) const {
+        // a round of pieces is 32 or 64 rows: the swizzle repeats
+        const uint32_t t = again(tid);
+        const int r = t / TL::NP, at = t % TL::NP;
+        const uint32_t ko = r * TL::ROW + 16 * (at ^ TL::swz_k(r)), vo = r * TL::ROW + 16 * (at ^ TL::swz_v(r));
+#pragma unroll
+        for (int n = 0; n < N; ++n) *(u32x4 *)(kt + ko + 16 * kLongNT * n) = k[n];
+#pragma unroll
+        for (int n = 0; n < N; ++n) *(u32x4 *)(vt + vo + 16 * kLongNT * n) = fix(r + kLongNT / TL::NP * n, at, v[n]);
+    }
+};
+template <>
+struct Staged<KEY_FP8, kDim> {
+    CodeRegs<1> k, v;
+    __device__ __forceinline__ void load(const uint8_t *kp, const uint8_t *vp, int tid) {
+        const uint32_t t = again(tid);
+        load_codes<1, kLongNT>(k, kp, t);
+        load_codes<1, kLongNT>(v, vp, t);
+    }
+    template <class F>
+    __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, float *ks, float *vs, int tid, F fix) const {
+        const uint32_t t = again(tid);
+        put_codes<1, kLongNT, true>(k, kt, ks, t, as_is);
+        put_codes<1, kLongNT, false>(v, vt, vs, t, fix);
+    }
+};
+
+template <int FMT, int D>
+__global__ __launch_bounds__(kLongNT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void attend_long_kernel(AttendArgs A) {
+    using TL = Tile<FMT, D>;
+    constexpr bool FP8 = FMT == KEY_FP8;
+    constexpr int S = 3, NW = kLongNT / 64;
+    static_assert(TL::SUB == 2, "two 32-entry tiles a tile");
+    __shared__ __align__(16) uint8_t sK[S][TL::BYTES], sV[S][TL::BYTES];
+    __shared__ float sS[FP8 ? S : 1][2][64];
+    __shared__ Special<D> sX[NW];
+    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
+    const int total = gridDim.x, x = blockIdx.x % 8, per8 = total / 8, rem = total % 8;
+    int id = (x < rem ? x * (per8 + 1) : rem * (per8 + 1) + (x - rem) * per8) + blockIdx.x / 8;
+    const int split = id % A.splits;
+    id /= A.splits;
+    const int blk = A.blocks - 1 - id % A.blocks, hk = (id / A.blocks) % A.n_kv, b = id / (A.blocks * A.n_kv);
+    const Req rq = request(A, b);
+    const int cols = rq.n * A.G, c0 = blk * 256;
+    if (c0 >= cols) return;
+    const Span sp = make_span<TL::E>(A, c0 / A.G, (min(c0 + 256, cols) - 1) / A.G, rq.n, rq.len);
+    const int per = (sp.count + A.splits - 1) / A.splits;
+    const int t0 = split * per, t1 = min(sp.count, t0 + per);
+    const bool idle = c0 + 32 * w >= cols;
+    const int R0 = c0 + 32 * w + j;
+    const Col col = make_col(A, R0, rq.row0, rq.n, rq.len);
+    u32x4 q[TL::QR];
+    load_q<FMT, D>(q, A, R0, rq.row0, hk, col.valid);
+    State<FMT, D> st;
+    st.clear();
+    clear_special(sX[w]);
+    __syncthreads();                                       // marks may come from any wave
+
+    // the next mapped tile from i on: its entries' places in the pools, and its index (i >= t1: none)
+    constexpr int row = FP8 ? kRowFp8 : TL::ROW;
+    const int64_t head = (int64_t)hk * kPage * row, step = (int64_t)A.n_kv * kPage * row;
+    const uint8_t *kp = (const uint8_t *)A.k + head, *vp = (const uint8_t *)A.v + head;
+    Staged<FMT, D> in;
+    auto fetch = [&](int i) {
+        for (; i < t1; ++i) {
+            const int page = __builtin_amdgcn_readfirstlane(page_of<FMT, D>(A, b, sp.at(i)));
+            if (page < 0) continue;
+            const int64_t at = page * step;
+            in.load(kp + at, vp + at, tid);
+            break;
+        }
+        return i;
+    };
+
+    // Tiles that some column of the workgroup sees only in part: masks are formed for these alone,
+    // and their values that are not finite are kept out of LDS (a product with a masked entry's 0
+    // would make them NaN): the thread that stages such a value marks the columns that see it.
+    const int i0 = c0 / A.G, i1 = (min(c0 + 256, cols) - 1) / A.G, base = rq.len - rq.n;
+    const int last = A.tree_mask ? rq.len : base + i1, from = last - (A.window - 1);   // all see [from, upto)
+    const int upto = max(0, A.tree_mask ? base : base + i0 + 1), most = A.tree_mask ? rq.len : base + i1 + 1;
+    const int whole0 = min(A.n_sink, upto) / TL::E;        // tiles [0, whole0) and [whole1, whole2) are seen whole
+    const int whole1 = (max(from, 0) + TL::E - 1) / TL::E, whole2 = upto / TL::E;
+    auto put = [&](int s, int t, bool edge) {
+        uint8_t *kt = sK[s], *vt = sV[s];
+        float *ks = sS[FP8 ? s : 0][0], *vs = sS[FP8 ? s : 0][1];
+        if (!edge) {
+            in.put(kt, vt, ks, vs, tid, as_is);
+            return;
+        }
+        in.put(kt, vt, ks, vs, tid, [&](int r, int piece, u32x4 y) {
+            uint32_t bad = 0;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) bad |= ((y[d] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+            if (bad == 0) return y;
+            const int entry = t * TL::E + r;
+#pragma unroll 1
+            for (int c = 0; c < 256 && entry < most; ++c) {
+                const Col k = make_col(A, c0 + c, rq.row0, rq.n, rq.len);
+                if (!k.valid || !(visible(k, t * TL::E, A.mask_ld) >> r & 1)) continue;
+                Special<D> &x = sX[c / 32];
+                x.any = 1;
+#pragma unroll 1
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t word = e < 2 ? y[0] : e < 4 ? y[1] : e < 6 ? y[2] : y[3];
+                    const uint32_t f = e & 1 ? word & 0xffff0000u : word << 16;
+                    if ((f & 0x7f800000u) != 0x7f800000u) continue;
+                    uint32_t *to = f & 0x007fffffu ? x.nan[c % 32] : f >> 31 ? x.down[c % 32] : x.up[c % 32];
+                    atomicOr(&to[piece / 4], 1u << (8 * (piece % 4) + e));
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) y[d] = finite_only<false>(y[d]);
+            return y;
+        });
+    };
+
+    // the scores of the 32-entry tile being worked on and of the next; the mask of their tile
+    SRegs<1> sa, sb;
+    uint64_t vis = ~0ull;
+    bool masked = false;
+    auto set_mask = [&](int t, bool edge) {
+        masked = false;
+        if (!edge) return;
+        vis = col.valid ? visible(col, t * TL::E, A.mask_ld) : ~0ull;
+        masked = __builtin_amdgcn_ballot_w64(vis != ~0ull) != 0;
+    };
+    // Scores formed (and, fp8, scaled) with their maximum mx; a mask changes both.
+    auto settle = [&](SRegs<1> &s, int sub, float mx) {
+        if (masked) {
+            hide<1>(s, vis >> (32 * sub));
+            mx = max_of<1>(s);
+        }
+        raise_max<FMT, D>(mx, A.c, st);
+    };
+    // The exponentials of one 32-entry tile beside the scores of the next, then its values; returns
+    // the scores' maximum.  Written in the order it is to run in, a matrix instruction and what
+    // fits beside it at a time: the values' reads and two entries' exponentials with each step of the
+    // first product, the scores' scales and maximum with the second.  The keys are read before the
+    // step that uses them (read_keys), behind the maximum's lane swap and branch.
+    uint32_t ko[TL::QR], vo[TL::DT];                      // the lane's reads in the current stages
+#pragma unroll
+    for (int i = 0; i < TL::QR; ++i) ko[i] = key_lane<FMT, D>() ^ (uint32_t)(32 * i);
+#pragma unroll
+    for (int t = 0; t < TL::DT; ++t) vo[t] = value_lane<FMT, D>() ^ (uint32_t)(64 * t);
+    auto move_keys = [&](int by) {
+#pragma unroll
+        for (int i = 0; i < TL::QR; ++i) ko[i] += (uint32_t)by;
+    };
+    auto move_values = [&](int by) {
+#pragma unroll
+        for (int t = 0; t < TL::DT; ++t) vo[t] += (uint32_t)by;
+    };
+    u32x4 ka[TL::QR];
+    auto read_keys = [&](int sub) {
+#pragma unroll
+        for (int i = 0; i < TL::QR; ++i) ka[i] = *(const u32x4 *)(sK[0] + 32 * sub * TL::ROW + ko[i]);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto advance = [&](SRegs<1> &now, int stage, int sub, SRegs<1> &then, int stage2, int sub2) {
+        const uint8_t *vt = sV[0] + 32 * sub * TL::ROW;
+        constexpr int QR = TL::QR, PV = 2 * TL::DT;       // matrix instructions of each product
+        constexpr int EX = 16 / QR;                       // entries a step of the first
+        u32x4 va[2][TL::DT];
+        u32x2 pk[2][2];
+        u32x4 ks4[FP8 ? 4 : 1], vs4[FP8 ? 4 : 1];
+        if constexpr (FP8) {
+            const int h = ln >> 5;
+#pragma unroll
+            for (int a = 0; a < 4; ++a) {
+                vs4[a] = *(const u32x4 *)(sS[stage][1] + 32 * sub + 8 * a + 4 * h);
+                ks4[a] = *(const u32x4 *)(sS[stage2][0] + 32 * sub2 + 8 * a + 4 * h);
+            }
+        }
+        float sum = st.l;
+        __builtin_amdgcn_s_setprio(1);                     // before the other wave's softmax: 330 -> 310 us
+        f32x16 s;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[v] = 0.f;
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            s = mma_bf16(ka[i], q[i], s);
+#pragma unroll
+            for (int x = i * PV / QR; x < (i + 1) * PV / QR; ++x) {
+                const uint8_t *row = vt + vo[x % TL::DT] + 16 * (x / TL::DT) * TL::ROW;
+                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)row));
+                const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4 *)(row + 8 * TL::ROW)));
+                va[x / TL::DT][x % TL::DT] = u32x4{a[0], a[1], c[0], c[1]};
+            }
+#pragma unroll
+            for (int v = EX * i; v < EX * (i + 1); v += 2) {
+                float p0 = __builtin_amdgcn_exp2f(fmaf(now[0][v], A.c, -st.mc));
+                float p1 = __builtin_amdgcn_exp2f(fmaf(now[0][v + 1], A.c, -st.mc));
+                sum += p0;
+                sum += p1;
+                if constexpr (FP8) {                      // a masked entry's scale may be anything
+                    const float y0 = p0 * __uint_as_float(vs4[v / 4][v % 4]), y1 = p1 * __uint_as_float(vs4[v / 4][v % 4 + 1]);
+                    p0 = p0 == 0.f ? 0.f : y0;
+                    p1 = p1 == 0.f ? 0.f : y1;
+                }
+                pk[v / 8][v % 8 / 4][v % 4 / 2] = pack_bf16(p0, p1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        st.l = sum;
+        float mx = kNegInf;
+        constexpr int MX = 16 / PV;
+#pragma unroll
+        for (int x = 0; x < PV; ++x) {
+            const u32x4 b = {pk[x / TL::DT][0][0], pk[x / TL::DT][0][1], pk[x / TL::DT][1][0], pk[x / TL::DT][1][1]};
+            st.o[x % TL::DT] = mma_bf16(va[x / TL::DT][x % TL::DT], b, st.o[x % TL::DT]);
+#pragma unroll
+            for (int v = MX * x; v < MX * (x + 1); ++v) {
+                if constexpr (FP8) s[v] *= __uint_as_float(ks4[v / 4][v % 4]);
+                mx = fmaxf(mx, s[v]);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_setprio(0);
+        then[0] = s;
+        return mx;
+    };
+    // A wave without columns runs the same loop, copying its share of the tiles.
+    auto run = [&](auto active) {
+        constexpr bool on = decltype(active)::value;
+        auto is_edge = [&](int t) { return t >= whole0 && (t < whole1 || t >= whole2); };
+        int i = fetch(t0), stage = 0;
+        if (i >= t1) return;
+        int t = sp.at(i);
+        bool edge = is_edge(t);
+        put(0, t, edge);
+        i = fetch(i + 1);                                  // the tile on its way
+        __syncthreads();
+        if constexpr (on) {
+            sa[0] = scores<FMT, D>(sK[0], key_lane<FMT, D>(), 0, q);
+            if constexpr (FP8) scale_scores<1>(sa, sS[0][0]);
+            set_mask(t, edge);
+            settle(sa, 0, max_of<1>(sa));
+            read_keys(1);
+        }
+        bool more;
+        do {
+            const int next = stage == S - 1 ? 0 : stage + 1, by = (next - stage) * TL::BYTES;
+            more = i < t1;
+            float mx = 0.f;
+            if constexpr (on) mx = advance(sa, stage, 0, sb, stage, 1);
+            if (more) {
+                t = sp.at(i);
+                edge = is_edge(t);
+                put(next, t, edge);
+                i = fetch(i + 1);
+                __syncthreads();
+            }
+            if constexpr (on) {
+                move_keys(by);
+                read_keys(0);
+                settle(sb, 1, mx);
+                mx = advance(sb, stage, 1, sa, next, 0);
+                move_values(by);
+                read_keys(1);
+                set_mask(t, edge && more);
+                if (!more) mx = kNegInf;                   // scores of no tile: they raise nothing
+                settle(sa, 0, mx);
+            }
+            stage = next;
+        } while (more);
+    };
+    if (idle) run(std::false_type());
+    else run(std::true_type());
+    // outputs through LDS, a stage for a wave's 32 columns, four waves at a time
+    static_assert(32 * D * 4 == TL::BYTES, "a stage holds a wave's outputs");
+#pragma unroll 1
+    for (int round = 0; round < NW / 4; ++round) {
+        __syncthreads();
+        if (idle || w / 4 != round) continue;
+        uint8_t *out = w % 4 < 3 ? sK[w % 4] : sV[0];
+        const float l = both_sum(st.l);
+        apply_special<FMT, D>(sX[w], st);
+        stage_o<FMT, D>(out, st);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int e = ln; e < 32 * (D / 4); e += 64) {
+            const int c = e / (D / 4), piece = e % (D / 4), R = c0 + 32 * w + c;
+            const float mc = __shfl(st.m, c), lc = __shfl(l, c);
+            if (R < cols) emit<FMT, D>(A, R, rq.row0, hk, split, piece, *stage_at<D>(out, c, piece), mc, lc);
+        }
     }
 }
 
@@ -888,11 +1240,13 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendArgs A) {
 
 template <int FMT, int D>
 hipError_t launch(const AttendArgs &a, hipStream_t s) {
-    if (a.blocks) {
-        attend_tile_kernel<FMT, D><<<dim3((unsigned)(a.splits * a.blocks * a.n_kv * a.B)), 256, 0, s>>>(a);
+    const unsigned wgs = (unsigned)(a.splits * std::max(a.blocks, 1) * a.n_kv * a.B);
+    if (a.blocks && a.columns == 256) {
+        if constexpr (FMT != KEY_F32) attend_long_kernel<FMT, D><<<dim3(wgs), kLongNT, 0, s>>>(a);
+    } else if (a.blocks) {
+        attend_tile_kernel<FMT, D><<<dim3(wgs), 256, 0, s>>>(a);
     } else {
-        const dim3 grid((unsigned)(a.splits * a.n_kv * a.B));
-        attend_split_kernel<FMT, D><<<grid, 256, 0, s>>>(a);
+        attend_split_kernel<FMT, D><<<dim3(wgs), 256, 0, s>>>(a);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;

@@ -635,27 +635,36 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
 #ifndef FM_ATTEND_TARGET
 #define FM_ATTEND_TARGET 512
 #endif
-#ifndef FM_ATTEND_MIN_TILES
-#define FM_ATTEND_MIN_TILES 8
+#ifndef FM_ATTEND_MIN_32
+#define FM_ATTEND_MIN_32 8
+#endif
+#ifndef FM_ATTEND_MIN_128
+#define FM_ATTEND_MIN_128 8
+#endif
+#ifndef FM_ATTEND_MIN_256
+#define FM_ATTEND_MIN_256 8
 #endif
 struct AttendPlan {
-    int blocks, splits;
+    int columns, blocks, splits;
     size_t ml_bytes, o_bytes;
 };
 AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
-    AttendPlan p{0, 1, 0, 0};
+    AttendPlan p{32, 0, 1, 0, 0};
     if (a->T == 0 || a->max_rows == 0) return p;
     const int G = a->n_heads / a->n_kv_heads;
     const int64_t cols = (int64_t)a->max_rows * G;
-    p.blocks = cols <= 32 ? 0 : (int)((cols + 127) / 128);
-    const int64_t rows = std::min<int64_t>(a->max_rows, (p.blocks ? 128 : 32) / G + 2);
+    if (cols > 32) {
+        p.columns = cols > 128 && kv->key_dtype != FM_F32 ? 256 : 128;
+        p.blocks = (int)((cols + p.columns - 1) / p.columns);
+    }
+    const int64_t rows = std::min<int64_t>(a->max_rows, p.columns / G + 2);
     const int E = fm::attend_tile_entries(key_fmt(kv->key_dtype));
     const int64_t seen = std::min<int64_t>(std::min<int64_t>(window, kv->max_seq_len) + rows +
                                                std::min<int64_t>(n_sink, kv->max_seq_len), kv->max_seq_len);
     const int64_t tiles = (seen + E - 1) / E;
     const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
     const int64_t want = (FM_ATTEND_TARGET + wgs - 1) / wgs;
-    p.splits = (int)std::max<int64_t>(1, std::min(want, tiles / FM_ATTEND_MIN_TILES));
+    p.splits = (int)std::max<int64_t>(1, std::min(want, tiles / (p.columns == 32 ? FM_ATTEND_MIN_32 : p.columns == 128 ? FM_ATTEND_MIN_128 : FM_ATTEND_MIN_256)));
     if (p.splits > 1) {
         const size_t parts = (size_t)p.splits * a->T * a->n_heads;
         p.ml_bytes = fm::align_up(parts * sizeof(float2), 256);
@@ -697,6 +706,7 @@ fm_status run_attend(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t
     x.n_sink = clamp32(n_sink);
     x.tree_mask = tree_mask;
     x.mask_ld = mask_ld;
+    x.columns = p.columns;
     x.blocks = p.blocks;
     x.splits = p.splits;
     x.part_ml = (float2 *)ws;

@@ -253,7 +253,8 @@ struct AttendArgs {
     int window, n_sink;       // entries back from a row's own (itself included); first entries
     const uint64_t *tree_mask;   // [T, mask_ld] or null
     int64_t mask_ld;
-    int blocks;               // 128-column blocks of a problem (tile kernel); 0: split kernel
+    int columns;              // columns of a workgroup: 32 (split kernel), 128 (tile) or 256 (long)
+    int blocks;               // such blocks of a problem; 0: split kernel
     int splits;               // parts the entries are split into
     float *part_o;            // [splits, T, n_heads, D]
     float2 *part_ml;          // [splits, T, n_heads]: maximum, sum
