@@ -263,50 +263,73 @@ __device__ __forceinline__ f32x16 scores(const uint8_t *kt, uint32_t lane, int s
     f32x16 s;
 #pragma unroll
     for (int v = 0; v < 16; ++v) s[v] = 0.f;
+    // eight reads go out before the first product waits for one: a wave may be alone on its SIMD
+    constexpr int U = TL::QR < 8 ? TL::QR : 8;
 #pragma unroll
-    for (int i = 0; i < TL::QR; ++i) {
-        const u32x4 a = *(const u32x4 *)(kt + 32 * sub * TL::ROW + (lane ^ (uint32_t)(32 * i)));
-        if constexpr (TL::F32) {
+    for (int i0 = 0; i0 < TL::QR; i0 += U) {
+        u32x4 a[U];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[c]), __uint_as_float(q[i][c]), s, 0, 0, 0);
-        } else {
-            s = mma_bf16(a, q[i], s);
+        for (int i = 0; i < U; ++i) a[i] = *(const u32x4 *)(kt + 32 * sub * TL::ROW + (lane ^ (uint32_t)(32 * (i0 + i))));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if constexpr (TL::F32) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    s = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[i][c]), __uint_as_float(q[i0 + i][c]), s, 0, 0, 0);
+            } else {
+                s = mma_bf16(a[i], q[i0 + i], s);
+            }
         }
     }
     return s;
 }
 
-// Column sums over the entries of NS 32-entry tiles: acc[d, column] += sum_e f(V[e, d]) P[e, column]
-// for the 32 values of tile t, f applied to the operand registers; lane: value_lane.
+// Column sums over the entries of NS 32-entry tiles: o[d, column] += sum_e f(V[e, d]) P[e, column],
+// f applied to the operand registers; lane: value_lane.  The values of 32 dims are read while the
+// ones before are weighed.
 template <int FMT, int D, int NS, class F>
-__device__ __forceinline__ f32x16 weigh(const uint8_t *vt, uint32_t lane, int t, const SRegs<NS> &p,
-                                        const PRegs<NS> &pk, f32x16 acc, F f) {
+__device__ __forceinline__ void weigh(const uint8_t *vt, uint32_t lane, const SRegs<NS> &p, const PRegs<NS> &pk,
+                                      f32x16 (&o)[D / 32], F f) {
     using TL = Tile<FMT, D>;
-    if constexpr (TL::F32) {
+    constexpr int N = TL::F32 ? 16 : 8 * NS;              // operand dwords
+    uint32_t x[2][N];
+    auto read = [&](uint32_t (&x)[N], int t) {
+        if constexpr (TL::F32) {
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            const int r = 8 * (v >> 2) + (v & 3);         // and 4 h, in lane
-            const uint32_t at = (lane ^ (uint32_t)(16 * TL::swz_v(r) ^ 128 * t)) + r * TL::ROW;
-            const uint32_t x = *(const uint32_t *)(vt + at);
-            acc = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f(x)), p[0][v], acc, 0, 0, 0);
-        }
-    } else {
-        const uint8_t *at = vt + (lane ^ (uint32_t)(64 * t));
-#pragma unroll
-        for (int sub = 0; sub < NS; ++sub)
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                // rows r, r + 8 of 32 sub + 16 ks ..: one swizzle for all
-                const uint8_t *row = at + (32 * sub + 16 * ks) * TL::ROW;
-                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)row));
-                const u32x2 b = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4 *)(row + 8 * TL::ROW)));
-                const u32x4 x = {f(a[0]), f(a[1]), f(b[0]), f(b[1])};
-                acc = mma_bf16(x, pk[sub][ks], acc);
+            for (int v = 0; v < 16; ++v) {
+                const int r = 8 * (v >> 2) + (v & 3);     // and 4 h, in lane
+                x[v] = *(const uint32_t *)(vt + (lane ^ (uint32_t)(16 * TL::swz_v(r) ^ 128 * t)) + r * TL::ROW);
             }
+        } else {
+            const uint8_t *at = vt + (lane ^ (uint32_t)(64 * t));
+#pragma unroll
+            for (int i = 0; i < 4 * NS; ++i) {            // rows 8 i and on: one swizzle for all
+                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (lds_s16x4 *)(at + 8 * i * TL::ROW)));
+                x[2 * i] = a[0];
+                x[2 * i + 1] = a[1];
+            }
+        }
+    };
+    read(x[0], 0);
+#pragma unroll
+    for (int t = 0; t < TL::DT; ++t) {
+        if (t + 1 < TL::DT) read(x[(t + 1) & 1], t + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t (&y)[N] = x[t & 1];
+        if constexpr (TL::F32) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v)
+                o[t] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(f(y[v])), p[0][v], o[t], 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2 * NS; ++i) {
+                const u32x4 a = {f(y[4 * i]), f(y[4 * i + 1]), f(y[4 * i + 2]), f(y[4 * i + 3])};
+                o[t] = mma_bf16(a, pk[i / 2][i % 2], o[t]);
+            }
+        }
     }
-    return acc;
 }
 
 template <int FMT, int NS>
@@ -525,14 +548,10 @@ __device__ __forceinline__ void add_values(const uint8_t *vt, uint32_t lane, con
     pack_p<FMT, NS>(p, pk);
     if (special) {
         mark_special<FMT, D, NS>(vt, p, vis, sp);
-#pragma unroll
-        for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-            st.o[t] = weigh<FMT, D, NS>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
+        weigh<FMT, D, NS>(vt, lane, p, pk, st.o, [](uint32_t x) { return finite_only<FMT == KEY_F32>(x); });
         return;
     }
-#pragma unroll
-    for (int t = 0; t < Tile<FMT, D>::DT; ++t)
-        st.o[t] = weigh<FMT, D, NS>(vt, lane, t, p, pk, st.o[t], [](uint32_t x) { return x; });
+    weigh<FMT, D, NS>(vt, lane, p, pk, st.o, [](uint32_t x) { return x; });
 }
 
 // Copy of a tile from the pool straight into LDS: instruction n of the tile moves 64 pieces.  The
@@ -629,27 +648,69 @@ __device__ __forceinline__ void stage_o(uint8_t *stage, const State<FMT, D> &st)
             *stage_at<D>(stage, j, 8 * t + 2 * a + h) = x;
         }
 }
-// Writes 4 values of column R (not yet divided by l) and, from its first piece, the statistics.
-template <int FMT, int D>
-__device__ __forceinline__ void emit(const AttendArgs &A, int R, int row0, int hk, int split, int piece, f32x4 o, float m,
-                                     float l) {
-    const int64_t row = row0 + R / A.G;
-    const int head = hk * A.G + R % A.G;
-    const int64_t rh = row * A.n_heads + head;
+// Where a column's outputs go, and what its sums are to be multiplied by: row (-1: nowhere), head.
+struct Dest {
+    int row, head;
+    float f;
+    int pad;
+};
+// The statistics of column R (m, l: of all its entries here), written; its sums' destination.
+__device__ __forceinline__ Dest finish_column(const AttendArgs &A, int R, int cols, int row0, int hk, int split, float m,
+                                              float l) {
+    Dest d{-1, 0, 1.f, 0};
+    if (R >= cols) return d;
+    const int i = R / A.G;
+    d.row = row0 + i;
+    d.head = hk * A.G + (R - i * A.G);
+    const int64_t rh = (int64_t)d.row * A.n_heads + d.head;
     if (A.splits > 1) {
-        const int64_t at = (int64_t)split * A.T * A.n_heads + rh;
-        *(f32x4 *)(A.part_o + at * D + 4 * piece) = o;
-        if (piece == 0) A.part_ml[at] = make_float2(m, l);
+        A.part_ml[(int64_t)split * A.T * A.n_heads + rh] = make_float2(m, l);
+    } else {
+        d.f = l == 0.f ? 0.f : 1.f / l;
+        if (A.lse) A.lse[rh] = l == 0.f ? kNegInf : m * A.scale + kLn2 * __builtin_amdgcn_logf(l);
+    }
+    return d;
+}
+// Four values of N columns each: all the LDS they come from is read before the first store.
+template <int FMT, int D, int N>
+__device__ __forceinline__ void emit(const AttendArgs &A, const Dest (&d)[N], int split, int piece, const f32x4 (&o)[N]) {
+    if (A.splits > 1) {
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (d[n].row >= 0)
+                *(f32x4 *)(A.part_o + (((int64_t)split * A.T + d[n].row) * A.n_heads + d[n].head) * D + 4 * piece) = o[n];
         return;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    if constexpr (FMT == KEY_F32) {
-        *(f32x4 *)((float *)A.out + row * A.out_ld + (int64_t)head * D + 4 * piece) = o * inv;
-    } else {
-        const u32x2 y = {pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-        *(u32x2 *)((uint16_t *)A.out + row * A.out_ld + (int64_t)head * D + 4 * piece) = y;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int64_t at = d[n].row * A.out_ld + d[n].head * D + 4 * piece;
+        const f32x4 x = o[n] * d[n].f;
+        if (d[n].row < 0) continue;
+        if constexpr (FMT == KEY_F32) *(f32x4 *)((float *)A.out + at) = x;
+        else *(u32x2 *)((uint16_t *)A.out + at) = u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
     }
-    if (piece == 0 && A.lse) A.lse[rh] = l == 0.f ? kNegInf : m * A.scale + kLn2 * __builtin_amdgcn_logf(l);
+}
+// A wave's 32 columns from c on, staged in LDS by itself: all of them out.
+template <int FMT, int D>
+__device__ __forceinline__ void emit_columns(const AttendArgs &A, const State<FMT, D> &st, int c, int cols, int row0,
+                                             int hk, int split, uint8_t *stage, Dest *dest) {
+    constexpr int P = D / 4, PER = 64 / P, N = 4;         // pieces of a column, columns at once
+    const int ln = __lane_id();
+    const float l = both_sum(st.l);
+    if (ln < 32) dest[ln] = finish_column(A, c + ln, cols, row0, hk, split, st.m, l);
+    stage_o<FMT, D>(stage, st);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+    for (int e = ln / P; e < 32; e += N * PER) {
+        Dest d[N];
+        f32x4 o[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            d[n] = dest[e + n * PER];
+            o[n] = *stage_at<D>(stage, e + n * PER, ln % P);
+        }
+        emit<FMT, D, N>(A, d, split, ln % P, o);
+    }
 }
 
 // ------------------------------------------------------------------ few columns
@@ -666,6 +727,7 @@ void attend_split_kernel(AttendArgs A) {
     constexpr int NI = TL::BYTES / 1024;
     __shared__ __align__(16) uint8_t sK[4][TL::BYTES], sV[FP8 ? 1 : 4][FP8 ? 16 : TL::BYTES];
     __shared__ float sS[FP8 ? 4 : 1][2][64], sM[4][32], sL[4][32];
+    __shared__ Dest sE[32];
     __shared__ Special<D> sX[4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
     const int split = blockIdx.x % A.splits, hk = (blockIdx.x / A.splits) % A.n_kv, b = blockIdx.x / (A.splits * A.n_kv);
@@ -675,12 +737,6 @@ void attend_split_kernel(AttendArgs A) {
     const Span sp = make_span<TL::E>(A, 0, rq.n - 1, rq.n, rq.len);
     const int per = (sp.count + A.splits - 1) / A.splits;
     const int t0 = split * per + w, t1 = min(sp.count, (split + 1) * per);
-    const Col col = make_col(A, j, rq.row0, rq.n, rq.len);
-    u32x4 q[TL::QR];
-    State<FMT, D> st;
-    load_q<FMT, D>(q, A, j, rq.row0, hk, col.valid);
-    st.clear();
-    clear_special(sX[w]);
     const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
     const uint32_t key0 = key_lane<FMT, D>(), value0 = value_lane<FMT, D>();
     uint8_t *kt = sK[w], *vt = FP8 ? sK[w] : sV[FP8 ? 0 : w];
@@ -716,6 +772,12 @@ void attend_split_kernel(AttendArgs A) {
         issue_k(sp.at(i));
         issue_v(sp.at(i));
     }
+    const Col col = make_col(A, j, rq.row0, rq.n, rq.len);
+    u32x4 q[TL::QR];
+    State<FMT, D> st;
+    load_q<FMT, D>(q, A, j, rq.row0, hk, col.valid);
+    st.clear();
+    clear_special(sX[w]);
     while (i < t1) {
         const int t = sp.at(i), s0 = t * TL::E;
         const int nx = seek(i + 4);
@@ -762,24 +824,59 @@ void attend_split_kernel(AttendArgs A) {
     apply_special<FMT, D>(sX[w], st);
     stage_o<FMT, D>(kt, st);
     __syncthreads();
-#pragma unroll 1
-    for (int e = tid; e < 32 * (D / 4); e += 256) {
-        const int c = e / (D / 4), piece = e % (D / 4);
-        if (c >= cols) continue;
-        float m = kNegInf, sum = 0.f;
+    if (tid < 32) {
+        float m = kNegInf, sum = 0.f, f[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) m = fmaxf(m, sM[k][c]);
-        f32x4 o = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < 4; ++k) m = fmaxf(m, sM[k][tid]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const float mk = sM[k][c];
-            const float f = mk == kNegInf ? 0.f : __builtin_amdgcn_exp2f((mk - m) * A.c);
-            if (sL[k][c] == 0.f) continue;                // nothing seen
-            sum += f * sL[k][c];
-            o += f * *stage_at<D>(sK[k], c, piece);
+            f[k] = sM[k][tid] == kNegInf ? 0.f : __builtin_amdgcn_exp2f((sM[k][tid] - m) * A.c);
+            sum += f[k] * sL[k][tid];
         }
-        emit<FMT, D>(A, c, rq.row0, hk, split, piece, o, m, sum);
+        sE[tid] = finish_column(A, tid, cols, rq.row0, hk, split, m, sum);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sM[k][tid] = f[k];
     }
+    __syncthreads();
+    constexpr int P = D / 4, N = 32 * P / 256;
+    Dest d[N];
+    f32x4 o[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int c = tid / P + n * (256 / P);
+        d[n] = sE[c];
+        o[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n] += sM[k][c] * *stage_at<D>(sK[k], c, tid % P);
+    }
+    emit<FMT, D, N>(A, d, split, tid % P, o);
+}
+
+// A workgroup's part of the entries, block of columns, kv head and request (b < 0: none).
+// Consecutive workgroups run on the chip's 8 XCDs in turn, each with an L2 of its own.  The blocks of
+// one (request, kv head) read the same tiles, so an XCD takes whole pairs, every eighth one (a
+// batch's requests differ in rows, its heads do not); with fewer than eight pairs, a run of blocks
+// each.  Later blocks see more entries and go first.
+struct Place {
+    int split, blk, hk, b;
+};
+__host__ __device__ __forceinline__ int64_t placed_workgroups(int pairs, int64_t per_pair) {
+    return pairs >= 8 ? 8 * ((pairs + 7) / 8 * per_pair) : pairs * per_pair;
+}
+__device__ __forceinline__ Place place_of(const AttendArgs &A) {
+    const int pairs = A.n_kv * A.B, per_pair = A.splits * A.blocks, x = blockIdx.x % 8, n = blockIdx.x / 8;
+    int pair, id;
+    if (pairs >= 8) {
+        pair = x + 8 * (n / per_pair);
+        id = n % per_pair;
+    } else {
+        const int total = gridDim.x, each = total / 8, rem = total % 8;
+        id = (x < rem ? x * (each + 1) : rem * (each + 1) + (x - rem) * each) + n;
+        pair = id / per_pair;
+        id %= per_pair;
+    }
+    if (pair >= pairs) return {0, 0, 0, -1};
+    return {id % A.splits, A.blocks - 1 - id / A.splits, pair % A.n_kv, pair / A.n_kv};
 }
 
 // ------------------------------------------------------------------ many columns
@@ -794,14 +891,11 @@ void attend_tile_kernel(AttendArgs A) {
     __shared__ __align__(16) uint8_t sK0[TL::BYTES], sV0[TL::BYTES], sK1[TL::BYTES], sV1[TL::BYTES];
     __shared__ float sS[FP8 ? 2 : 1][2][64];
     __shared__ Special<D> sX[4];
+    __shared__ Dest sE[4][32];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
-    // consecutive workgroups run on the chip's 8 XCDs in turn: each gets a contiguous run of
-    // problems, so the blocks that share a kv head's tiles share an L2, the longest first
-    const int total = gridDim.x, x = blockIdx.x % 8, per8 = total / 8, rem = total % 8;
-    int id = (x < rem ? x * (per8 + 1) : rem * (per8 + 1) + (x - rem) * per8) + blockIdx.x / 8;
-    const int split = id % A.splits;
-    id /= A.splits;
-    const int blk = A.blocks - 1 - id % A.blocks, hk = (id / A.blocks) % A.n_kv, b = id / (A.blocks * A.n_kv);
+    const Place at = place_of(A);
+    if (at.b < 0) return;
+    const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;
     const Req rq = request(A, b);
     const int cols = rq.n * A.G, c0 = blk * 128;
     if (c0 >= cols) return;
@@ -809,13 +903,10 @@ void attend_tile_kernel(AttendArgs A) {
     const int per = (sp.count + A.splits - 1) / A.splits;
     const int t0 = split * per, t1 = min(sp.count, t0 + per);
     const int R = c0 + 32 * w + j;
-    const Col col = make_col(A, R, rq.row0, rq.n, rq.len);
     const bool idle = c0 + 32 * w >= cols;
+    Col col;
     u32x4 q[TL::QR];
-    load_q<FMT, D>(q, A, R, rq.row0, hk, col.valid);
     State<FMT, D> st;
-    st.clear();
-    clear_special(sX[w]);
     const uint32_t key0 = key_lane<FMT, D>(), value0 = value_lane<FMT, D>();
     const uint8_t *kp = (const uint8_t *)A.k, *vp = (const uint8_t *)A.v;
     int page = -1;
@@ -829,15 +920,15 @@ void attend_tile_kernel(AttendArgs A) {
     };
     CodeRegs<FP8 ? 2 : 1> kc, vc;
     auto issue = [&](uint8_t *kt, uint8_t *vt, int t) {
-        const int64_t at = tile_at<FMT, D>(A, page, hk, t);
+        const int64_t ofs = tile_at<FMT, D>(A, page, hk, t);
         if constexpr (FP8) {
-            load_codes<2, 256>(kc, kp + at, again(tid));
-            load_codes<2, 256>(vc, vp + at, again(tid));
+            load_codes<2, 256>(kc, kp + ofs, again(tid));
+            load_codes<2, 256>(vc, vp + ofs, again(tid));
         } else {
 #pragma unroll
-            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + at, kt, NI * w + n);
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + ofs, kt, NI * w + n);
 #pragma unroll
-            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(vp + at, vt, NI * w + n);
+            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(vp + ofs, vt, NI * w + n);
         }
     };
     auto work = [&](const uint8_t *kt, const uint8_t *vt, const float *ks, const float *vs, int t) {
@@ -869,24 +960,18 @@ void attend_tile_kernel(AttendArgs A) {
         work(kt, vt, sS[FP8 ? stage : 0][0], sS[FP8 ? stage : 0][1], t);
     };
     if (i < t1) issue(sK0, sV0, sp.at(i));
+    col = make_col(A, R, rq.row0, rq.n, rq.len);          // beside the first tile's copy
+    load_q<FMT, D>(q, A, R, rq.row0, hk, col.valid);
+    st.clear();
+    clear_special(sX[w]);
     while (i < t1) {
         step(sK0, sV0, sK1, sV1, 0);
         if (i >= t1) break;
         step(sK1, sV1, sK0, sV0, FP8 ? 1 : 0);
     }
     __syncthreads();
-    uint8_t *stage = w == 0 ? sK0 : w == 1 ? sV0 : w == 2 ? sK1 : sV1;
-    const float l = both_sum(st.l);
     apply_special<FMT, D>(sX[w], st);
-    stage_o<FMT, D>(stage, st);
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-    for (int e = ln; e < 32 * (D / 4); e += 64) {
-        const int c = e / (D / 4), piece = e % (D / 4);
-        const float mc = __shfl(st.m, c), lc = __shfl(l, c);
-        if (c0 + 32 * w + c < cols)
-            emit<FMT, D>(A, c0 + 32 * w + c, rq.row0, hk, split, piece, *stage_at<D>(stage, c, piece), mc, lc);
-    }
+    emit_columns<FMT, D>(A, st, c0 + 32 * w, cols, rq.row0, hk, split, w == 0 ? sK0 : w == 1 ? sV0 : w == 2 ? sK1 : sV1, sE[w]);
 }
 
 // ------------------------------------------------------------------ many columns, long runs
@@ -947,12 +1032,11 @@ void attend_long_kernel(AttendArgs A) {
     __shared__ __align__(16) uint8_t sK[S][TL::BYTES], sV[S][TL::BYTES];
     __shared__ float sS[FP8 ? S : 1][2][64];
     __shared__ Special<D> sX[NW];
+    __shared__ Dest sE[NW][32];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
-    const int total = gridDim.x, x = blockIdx.x % 8, per8 = total / 8, rem = total % 8;
-    int id = (x < rem ? x * (per8 + 1) : rem * (per8 + 1) + (x - rem) * per8) + blockIdx.x / 8;
-    const int split = id % A.splits;
-    id /= A.splits;
-    const int blk = A.blocks - 1 - id % A.blocks, hk = (id / A.blocks) % A.n_kv, b = id / (A.blocks * A.n_kv);
+    const Place at = place_of(A);
+    if (at.b < 0) return;
+    const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;
     const Req rq = request(A, b);
     const int cols = rq.n * A.G, c0 = blk * 256;
     if (c0 >= cols) return;
@@ -1186,52 +1270,55 @@ void attend_long_kernel(AttendArgs A) {
     for (int round = 0; round < NW / 4; ++round) {
         __syncthreads();
         if (idle || w / 4 != round) continue;
-        uint8_t *out = w % 4 < 3 ? sK[w % 4] : sV[0];
-        const float l = both_sum(st.l);
         apply_special<FMT, D>(sX[w], st);
-        stage_o<FMT, D>(out, st);
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int e = ln; e < 32 * (D / 4); e += 64) {
-            const int c = e / (D / 4), piece = e % (D / 4), R = c0 + 32 * w + c;
-            const float mc = __shfl(st.m, c), lc = __shfl(l, c);
-            if (R < cols) emit<FMT, D>(A, R, rq.row0, hk, split, piece, *stage_at<D>(out, c, piece), mc, lc);
-        }
+        emit_columns<FMT, D>(A, st, c0 + 32 * w, cols, rq.row0, hk, split, w % 4 < 3 ? sK[w % 4] : sV[0], sE[w]);
     }
 }
 
 // ------------------------------------------------------------------ joining the parts
-// One wave a (row, head): D values, the splits' parts weighed by e^(m - max).
+// One wave a (row, head): lane s weighs part s by e^(m - max), then each lane sums its D / 64
+// values over the parts, eight parts' loads at a time.
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void attend_merge_kernel(AttendArgs A) {
+    constexpr int W = D / 64;
     const int ln = __lane_id();
-    const int b = blockIdx.y;
-    const Req rq = request(A, b);
+    const Req rq = request(A, blockIdx.y);
     const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int i = (int)(e / A.n_heads), head = (int)(e % A.n_heads);
     if (i >= rq.n) return;
     const int64_t row = rq.row0 + i, rh = row * A.n_heads + head, all = (int64_t)A.T * A.n_heads;
-    float m = kNegInf;
-    for (int s = 0; s < A.splits; ++s) {
-        const float2 x = A.part_ml[s * all + rh];
-        if (x.y != 0.f) m = fmaxf(m, x.x);
-    }
-    float l = 0.f, o[D / 64];
+    const float2 x = ln < A.splits ? A.part_ml[ln * all + rh] : make_float2(kNegInf, 0.f);
+    float m = x.y == 0.f ? kNegInf : x.x;                 // a part that saw nothing left no sums
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) o[k] = 0.f;
-    for (int s = 0; s < A.splits; ++s) {
-        const float2 x = A.part_ml[s * all + rh];
-        if (x.y == 0.f) continue;                         // nothing seen
-        const float f = x.x == kNegInf ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * A.c);
-        l += f * x.y;
-        const float *src = A.part_o + (s * all + rh) * D;
+    for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o));
+    const float f = x.y == 0.f || x.x == kNegInf ? 0.f : __builtin_amdgcn_exp2f((x.x - m) * A.c);
+    float l = f * x.y;
 #pragma unroll
-        for (int k = 0; k < D / 64; ++k) o[k] += f * src[(D / 64) * ln + k];
+    for (int o = 1; o < 64; o <<= 1) l += __shfl_xor(l, o);
+    float o[W];
+#pragma unroll
+    for (int k = 0; k < W; ++k) o[k] = 0.f;
+    const float *src = A.part_o + rh * D + W * ln;
+    constexpr int U = 8;
+    for (int s0 = 0; s0 < A.splits; s0 += U) {
+        float v[U][W];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float *p = src + min(s0 + u, A.splits - 1) * all * D;
+#pragma unroll
+            for (int k = 0; k < W; ++k) v[u][k] = p[k];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float g = s0 + u < A.splits ? __shfl(f, s0 + u) : 0.f;
+#pragma unroll
+            for (int k = 0; k < W; ++k) o[k] += g == 0.f ? 0.f : g * v[u][k];
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t at = row * A.out_ld + (int64_t)head * D + (D / 64) * ln;
+    const int64_t at = row * A.out_ld + (int64_t)head * D + W * ln;
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
+    for (int k = 0; k < W; ++k) {
         if constexpr (FMT == KEY_F32) ((float *)A.out)[at + k] = o[k] * inv;
         else ((uint16_t *)A.out)[at + k] = (uint16_t)pack_bf16(o[k] * inv, 0.f);
     }
@@ -1240,7 +1327,8 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendArgs A) {
 
 template <int FMT, int D>
 hipError_t launch(const AttendArgs &a, hipStream_t s) {
-    const unsigned wgs = (unsigned)(a.splits * std::max(a.blocks, 1) * a.n_kv * a.B);
+    const unsigned wgs = a.blocks ? (unsigned)placed_workgroups(a.n_kv * a.B, (int64_t)a.splits * a.blocks)
+                                  : (unsigned)(a.splits * a.n_kv * a.B);
     if (a.blocks && a.columns == 256) {
         if constexpr (FMT != KEY_F32) attend_long_kernel<FMT, D><<<dim3(wgs), kLongNT, 0, s>>>(a);
     } else if (a.blocks) {

@@ -629,21 +629,12 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     return FM_OK;
 }
 
-// The kernel and the split of the entries: up to 32 columns (rows x heads of a kv head) take the
-// kernel whose waves stream tiles of their own, more take 128-column blocks.  Entries are split
-// over more workgroups while there are fewer than kAttendTarget and each keeps kAttendMinTiles.
-#ifndef FM_ATTEND_TARGET
-#define FM_ATTEND_TARGET 512
-#endif
-#ifndef FM_ATTEND_MIN_32
-#define FM_ATTEND_MIN_32 8
-#endif
-#ifndef FM_ATTEND_MIN_128
-#define FM_ATTEND_MIN_128 8
-#endif
-#ifndef FM_ATTEND_MIN_256
-#define FM_ATTEND_MIN_256 8
-#endif
+// The kernel and the split of the entries.  Up to 32 columns (rows x heads of a kv head) take the
+// kernel whose waves stream tiles of their own, up to 128 (float32: any number) 128-column blocks,
+// more 256-column blocks.  The entries of a block are split over S workgroups where that ends
+// sooner by this estimate (us; measured per kernel with head_dim 128): rounds of workgroups over
+// the chip x (tiles a workgroup x time a tile + a workgroup's start and end), and for S > 1 the
+// joining launch and its traffic.
 struct AttendPlan {
     int columns, blocks, splits;
     size_t ml_bytes, o_bytes;
@@ -652,9 +643,10 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     AttendPlan p{32, 0, 1, 0, 0};
     if (a->T == 0 || a->max_rows == 0) return p;
     const int G = a->n_heads / a->n_kv_heads;
+    const bool f32 = kv->key_dtype == FM_F32, fp8 = kv->key_dtype == FM_FP8_E4M3_SCALED132;
     const int64_t cols = (int64_t)a->max_rows * G;
     if (cols > 32) {
-        p.columns = cols > 128 && kv->key_dtype != FM_F32 ? 256 : 128;
+        p.columns = cols > 128 && !f32 ? 256 : 128;
         p.blocks = (int)((cols + p.columns - 1) / p.columns);
     }
     const int64_t rows = std::min<int64_t>(a->max_rows, p.columns / G + 2);
@@ -663,8 +655,19 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
                                                std::min<int64_t>(n_sink, kv->max_seq_len), kv->max_seq_len);
     const int64_t tiles = (seen + E - 1) / E;
     const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
-    const int64_t want = (FM_ATTEND_TARGET + wgs - 1) / wgs;
-    p.splits = (int)std::max<int64_t>(1, std::min(want, tiles / (p.columns == 32 ? FM_ATTEND_MIN_32 : p.columns == 128 ? FM_ATTEND_MIN_128 : FM_ATTEND_MIN_256)));
+    const int slots = p.columns == 128 ? 512 : 256;            // workgroups the chip holds at once
+    const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? (f32 ? 5.8 : 1.7) : 2.4) *
+                        kv->head_dim / 128.0, ends = 6.0;
+    const double part = 8e-6 / 4.0 * a->T * a->n_heads * kv->head_dim;   // a split's sums, written and read, at 4 TB/s
+    double best = 0;
+    for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, tiles / 2)); ++s) {   // 64: the joining wave's lanes
+        const double t = (double)((wgs * s + slots - 1) / slots) * ((double)((tiles + s - 1) / s) * tile + ends) +
+                         (s > 1 ? 5.0 + s * part : 0.0);
+        if (s == 1 || t < best) {
+            best = t;
+            p.splits = (int)s;
+        }
+    }
     if (p.splits > 1) {
         const size_t parts = (size_t)p.splits * a->T * a->n_heads;
         p.ml_bytes = fm::align_up(parts * sizeof(float2), 256);
