@@ -47,10 +47,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *sh, int64_t &t
 
 // First entry of the call naming each request: later ones with the same request are refused.
 __device__ __forceinline__ void claim(const CacheArgs &A, const int32_t *req, int32_t *claims) {
+    const int mine = threadIdx.x < A.n ? req[threadIdx.x] : -1;      // on its way meanwhile
     for (int b = threadIdx.x; b < A.B; b += kPlanNT) claims[b] = INT32_MAX;
     __syncthreads();
     for (int i = threadIdx.x; i < A.n; i += kPlanNT) {
-        const int r = req[i];
+        const int r = i < kPlanNT ? mine : req[i];
         if (r >= 0 && r < A.B) atomicMin(&claims[r], i);
     }
     __syncthreads();
@@ -60,15 +61,23 @@ __device__ __forceinline__ int length_of(const CacheArgs &A, int r) {
     return (int)max((int64_t)0, min((int64_t)A.seq_lens[r], A.bt_ld * kPage));
 }
 
-// One reference less; the page goes into the bitmap when it was the last.
-__device__ __forceinline__ void drop(const CacheArgs &A, int page, uint32_t *freed) {
+// One reference less; the page goes into the bitmap when it was the last, and any is set.
+__device__ __forceinline__ void drop(const CacheArgs &A, int page, uint32_t *freed, int *any) {
     const int before = atomicSub(&A.ref[page], 1);
-    if (before == 1) atomicOr(&freed[page >> 5], 1u << (page & 31));
-    else if (before <= 0) atomicAdd(&A.ref[page], 1);     // was free already: left as it was
+    if (before == 1) {
+        atomicOr(&freed[page >> 5], 1u << (page & 31));
+        *any = 1;
+    } else if (before <= 0) {
+        atomicAdd(&A.ref[page], 1);                       // was free already: left as it was
+    }
 }
 
 // The bitmap's pages onto the stack, which holds `held` of them, in page order.
-__device__ __forceinline__ void push(const CacheArgs &A, const uint32_t *freed, int64_t held, int64_t *sh) {
+__device__ __forceinline__ void push(const CacheArgs &A, const uint32_t *freed, int any, int64_t held, int64_t *sh) {
+    if (!any) {
+        if (threadIdx.x == 0) *A.n_free = (int32_t)held;
+        return;
+    }
     const int words = (int)((A.n_phys + 31) / 32), per = (words + kPlanNT - 1) / kPlanNT;
     const int w0 = min(words, (int)threadIdx.x * per), w1 = min(words, w0 + per);
     int mine = 0;
@@ -87,10 +96,9 @@ __device__ __forceinline__ void clear_freed(const CacheArgs &A, uint32_t *freed)
     for (int w = threadIdx.x; w < (A.n_phys + 31) / 32; w += kPlanNT) freed[w] = 0;
 }
 
-// Threads per entry when the workgroup's threads are shared among n entries: a power of two of
-// whole waves.
+// Threads per entry when the workgroup's threads are shared among n entries: a power of two.
 __device__ __forceinline__ int team_size(int n) {
-    int t = 64;
+    int t = 16;
     while (t < kPlanNT && (int64_t)t * 2 * n <= kPlanNT) t *= 2;
     return t;
 }
@@ -126,18 +134,28 @@ __global__ __launch_bounds__(kPlanNT) void cache_release_kernel(CacheArgs A) {
     __shared__ int32_t claims[kCacheMaxRequests];
     __shared__ uint8_t bad[kCacheMaxRequests];
     __shared__ int64_t sh[kPlanNT / 64];
+    __shared__ int any;
+    const int64_t held = max((int64_t)0, min((int64_t)*A.n_free, A.n_phys));
+    const int team = team_size(A.n), lane = threadIdx.x % team, first = threadIdx.x / team, teams = kPlanNT / team;
+    // entry i's request, its length and where it is cut; with an entry a team they stay in
+    // registers from the verdict to the release
+    int r = -1, len = 0, cut = 0;
+    auto look = [&](int i) {
+        r = A.req[i];
+        cut = COMPACT ? A.start[i] + A.n_keep[i] : A.new_len ? A.new_len[i] : 0;
+        len = r >= 0 && r < A.B ? length_of(A, r) : -1;
+    };
+    if (first < A.n) look(first);
     clear_freed(A, freed);
+    if (threadIdx.x == 0) any = 0;
     for (int i = threadIdx.x; i < A.n; i += kPlanNT) bad[i] = 0;
     claim(A, A.req, claims);
-    const int team = team_size(A.n), lane = threadIdx.x % team, first = threadIdx.x / team, teams = kPlanNT / team;
-    auto cut_of = [&](int i) { return COMPACT ? A.start[i] + A.n_keep[i] : A.new_len ? A.new_len[i] : 0; };
     for (int i = first; i < A.n; i += teams) {
-        const int r = A.req[i];
-        bool good = r >= 0 && r < A.B && claims[r] == i;
+        if (i != first) look(i);
+        bool good = len >= 0 && claims[r] == i;
         if (good) {
-            const int len = length_of(A, r);
             if constexpr (COMPACT) good = keep_is_good(A, i, r, len, lane, team);
-            else good = cut_of(i) >= 0 && cut_of(i) <= len;
+            else good = cut >= 0 && cut <= len;
         }
         if (!good) bad[i] = 1;
     }
@@ -146,19 +164,18 @@ __global__ __launch_bounds__(kPlanNT) void cache_release_kernel(CacheArgs A) {
         const bool good = !bad[i];
         if (lane == 0 && A.ok) A.ok[i] = good;
         if (!good) continue;
-        const int r = A.req[i], cut = cut_of(i);
+        if (teams < A.n) look(i);
         int32_t *row = A.block_table + (int64_t)r * A.bt_ld;
-        const int c1 = pages_of(length_of(A, r));
+        const int c1 = pages_of(len);
         for (int c = pages_of(cut) + lane; c < c1; c += team) {
             const int page = row[c];
             row[c] = -1;
-            if (page >= 0 && page < A.n_phys) drop(A, page, freed);
+            if (page >= 0 && page < A.n_phys) drop(A, page, freed, &any);
         }
+        if (lane == 0) A.seq_lens[r] = cut;               // read by this team alone
     }
-    __syncthreads();                                       // the lengths are read
-    for (int i = threadIdx.x; i < A.n; i += kPlanNT)
-        if (!bad[i]) A.seq_lens[A.req[i]] = cut_of(i);
-    push(A, freed, max((int64_t)0, min((int64_t)*A.n_free, A.n_phys)), sh);
+    __syncthreads();
+    push(A, freed, any, held, sh);
 }
 
 // Pages for forks (FORK) and for growth.  plan[i] receives what the copy needs: a fork's length
@@ -168,32 +185,37 @@ __global__ __launch_bounds__(kPlanNT) void cache_plan_kernel(CacheArgs A) {
     __shared__ uint32_t freed[FORK ? 1 : kCacheMaxPages / 32];
     __shared__ int32_t claims[kCacheMaxRequests];
     __shared__ int64_t sh[kPlanNT / 64];
+    __shared__ int4 plans[kPlanNT];                       // of the call's entries, where they fit
+    __shared__ int any, taken;
+    const bool fits = A.n <= kPlanNT;
+    const int32_t *req = FORK ? A.dst : A.req;
     const int64_t have = max((int64_t)0, min((int64_t)*A.n_free, A.n_phys));
     if constexpr (!FORK) clear_freed(A, freed);
-    claim(A, FORK ? A.dst : A.req, claims);
+    if (threadIdx.x == 0) any = taken = 0;
+    claim(A, req, claims);
     // what each entry needs, before anything is changed; its first page's rank goes to plan[i].w
-    int64_t base = 0, taken = 0;
+    int64_t base = 0;
     for (int i0 = 0; i0 < A.n; i0 += kPlanNT) {
         const int i = i0 + threadIdx.x;
         bool good = false;
-        int need = 0, len = 0, cow = -1;
+        int need = 0, len = 0, cow = -1, r = -1, old = 0;
         if (i < A.n) {
-            const int r = FORK ? A.dst[i] : A.req[i];
-            if (r >= 0 && r < A.B && claims[r] == i) {
+            r = req[i];
+            if (r >= 0 && r < A.B) {
                 if constexpr (FORK) {
                     const int s = A.src[i];
-                    if (s >= 0 && s < A.B && s != r && A.seq_lens[r] == 0) {
+                    if (s >= 0 && s < A.B && s != r) {
                         len = length_of(A, s);
                         need = A.deep ? pages_of(len) : len % kPage != 0;
-                        good = true;
+                        good = A.seq_lens[r] == 0 && claims[r] == i;
                     }
                 } else {
-                    const int old = length_of(A, r), now = A.new_len[i];
-                    if (now >= old && pages_of(now) <= A.bt_ld) {
+                    old = length_of(A, r);
+                    len = A.new_len[i];
+                    if (claims[r] == i && len >= old && pages_of(len) <= A.bt_ld) {
                         good = true;
-                        len = now;
-                        need = pages_of(now) - pages_of(old);
-                        if (old % kPage && now > old) {
+                        need = pages_of(len) - pages_of(old);
+                        if (old % kPage && len > old) {
                             const int page = A.block_table[(int64_t)r * A.bt_ld + old / kPage];
                             if (page >= 0 && page < A.n_phys && A.ref[page] > 1) cow = page;
                         }
@@ -205,23 +227,22 @@ __global__ __launch_bounds__(kPlanNT) void cache_plan_kernel(CacheArgs A) {
         int64_t total;
         const int64_t mine = base + block_scan(good ? need : 0, sh, total);
         good = good && mine + need <= have;
-        // granted entries are a prefix of the valid ones
-        int64_t got;
-        block_scan(good ? need : 0, sh, got);
-        taken += got;
         base += total;
+        // granted entries are a prefix of the valid ones: the last one's end is what is taken
+        if (good) atomicMax(&taken, (int)(mine + need));
         if (i < A.n) {
-            A.plan[i] = make_int4(good ? len : -1, cow, -1, good ? (int)mine : 0);
+            const int4 p = make_int4(good ? len : -1, cow, -1, good ? (int)mine : 0);
+            if (fits) plans[i] = p;
+            A.plan[i] = p;
             if (A.ok) A.ok[i] = good;
         }
     }
     __syncthreads();
-    __threadfence_block();
     const int team = team_size(A.n), lane = threadIdx.x % team;
     for (int i = threadIdx.x / team; i < A.n; i += kPlanNT / team) {
-        const int4 p = A.plan[i];
+        const int4 p = fits ? plans[i] : A.plan[i];
         if (p.x < 0) continue;
-        const int r = FORK ? A.dst[i] : A.req[i];
+        const int r = req[i];
         int32_t *row = A.block_table + (int64_t)r * A.bt_ld;
         const int old = FORK ? 0 : length_of(A, r);
         // fresh pages go to cells c0 .. c1 - 1; a copied one to the cell before, from the first rank
@@ -234,19 +255,19 @@ __global__ __launch_bounds__(kPlanNT) void cache_plan_kernel(CacheArgs A) {
             if (fine) A.ref[page] = 1;
             if (cow && c == c0 - 1) {
                 A.plan[i].z = fine ? page : -1;
-                drop(A, p.y, freed);
+                drop(A, p.y, freed, &any);
             }
         }
     }
-    __syncthreads();
+    __syncthreads();                                       // the lengths are read
     for (int i = threadIdx.x; i < A.n; i += kPlanNT) {
-        const int len = A.plan[i].x;
-        if (len >= 0) A.seq_lens[FORK ? A.dst[i] : A.req[i]] = len;
+        const int len = fits ? plans[i].x : A.plan[i].x;
+        if (len >= 0) A.seq_lens[req[i]] = len;
     }
     if constexpr (FORK) {
         if (threadIdx.x == 0) *A.n_free = (int32_t)(have - taken);
     } else {
-        push(A, freed, have - taken, sh);
+        push(A, freed, any, have - taken, sh);
     }
 }
 
@@ -259,7 +280,16 @@ __device__ __forceinline__ void copy_part(const CacheArgs &A, int pool, int from
     const int64_t bytes = page_bytes(A, pool), n = bytes / 16;
     const u32x4 *src = (const u32x4 *)(A.pool[pool] + from * bytes);
     u32x4 *dst = (u32x4 *)(A.pool[pool] + to * bytes);
-    for (int64_t x = part * 256 + threadIdx.x; x < n; x += parts * 256) dst[x] = src[x];
+    constexpr int U = 8;                                   // loads in flight a thread
+    for (int64_t x = part * 256 + threadIdx.x; x < n; x += (int64_t)U * parts * 256) {
+        u32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (x + u * parts * 256 < n) v[u] = src[x + u * parts * 256];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (x + u * parts * 256 < n) dst[x + u * parts * 256] = v[u];
+    }
 }
 
 // The data of forks and growths: workgroup (part of a page, entry, pool).

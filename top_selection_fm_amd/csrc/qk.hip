@@ -24,8 +24,10 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <bool F32> struct Io {
     static constexpr int VEC = F32 ? 4 : 8, SIZE = F32 ? 4 : 2;
-    __device__ static __forceinline__ void load(float *x, const void *p, int64_t at) {
-        const u32x4 r = *(const u32x4 *)((const uint8_t *)p + at * SIZE);
+    __device__ static __forceinline__ u32x4 raw(const void *p, int64_t at) {
+        return *(const u32x4 *)((const uint8_t *)p + at * SIZE);
+    }
+    __device__ static __forceinline__ void widen(float *x, const u32x4 &r) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (F32) {
@@ -69,6 +71,19 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs A) {
     __shared__ float2 cs[FM_HEAD_DIM / 2];
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid % L, e0 = VEC * lane;
     const int half = A.rope_dim / 2;
+    const int heads = A.n_heads + A.n_kv * (A.store ? 2 : 1), by = gridDim.y * GROUPS;
+    // head i of the row: q's, then k's, then v's
+    auto fetch = [&](int i) {
+        const bool is_q = i < A.n_heads, is_v = i >= A.n_heads + A.n_kv;
+        const int h = is_q ? i : is_v ? i - A.n_heads - A.n_kv : i - A.n_heads;
+        return IO::raw(is_q ? A.q : is_v ? A.v : A.k, t * (is_q ? A.q_ld : is_v ? A.v_ld : A.k_ld) + (int64_t)h * D + e0);
+    };
+    // the first head and the weights are on their way while the angles are formed
+    int i = blockIdx.y * GROUPS + tid / L;
+    u32x4 next = {0u, 0u, 0u, 0u}, qw = next, kw = next;
+    if (i < heads) next = fetch(i);
+    if (A.q_norm) qw = IO::raw(A.q_norm, e0);
+    if (A.k_norm) kw = IO::raw(A.k_norm, e0);
     if (tid < half) {
         double turns = (double)A.pos[t] * A.turns[tid];
         turns -= rint(turns);
@@ -89,19 +104,18 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs A) {
         }
     }
     __syncthreads();
-    const int heads = A.n_heads + A.n_kv * (A.store ? 2 : 1);
     const bool turned = e0 >= A.rope_first && e0 < A.rope_first + A.rope_dim;
-    for (int i = blockIdx.y * GROUPS + tid / L; i < heads; i += gridDim.y * GROUPS) {
+    for (; i < heads; i += by) {
+        float x[VEC];
+        IO::widen(x, next);
+        if (i + by < heads) next = fetch(i + by);
         const bool is_q = i < A.n_heads, is_v = i >= A.n_heads + A.n_kv;
         const int h = is_q ? i : is_v ? i - A.n_heads - A.n_kv : i - A.n_heads;
         if (is_v && cell < 0) continue;
-        float x[VEC];
-        IO::load(x, is_q ? A.q : is_v ? A.v : A.k, t * (is_q ? A.q_ld : is_v ? A.v_ld : A.k_ld) + (int64_t)h * D + e0);
         if (!is_v) {
-            const void *g = is_q ? A.q_norm : A.k_norm;
-            if (g) {
+            if (is_q ? A.q_norm : A.k_norm) {
                 float w[VEC], ss = 0.f;
-                IO::load(w, g, e0);
+                IO::widen(w, is_q ? qw : kw);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) ss = fmaf(x[j], x[j], ss);
                 const float inv = 1.0f / sqrtf(lanes_sum<L>(ss) / (float)D + A.eps);
