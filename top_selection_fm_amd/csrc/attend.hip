@@ -1159,17 +1159,16 @@ void attend_long_kernel(AttendArgs A) {
         constexpr int EX = 16 / QR;                       // entries a step of the first
         u32x4 va[2][TL::DT];
         u32x2 pk[2][2];
-        u32x4 ks4[FP8 ? 4 : 1], vs4[FP8 ? 4 : 1];
-        if constexpr (FP8) {
-            const int h = ln >> 5;
-#pragma unroll
-            for (int a = 0; a < 4; ++a) {
-                vs4[a] = *(const u32x4 *)(sS[stage][1] + 32 * sub + 8 * a + 4 * h);
-                ks4[a] = *(const u32x4 *)(sS[stage2][0] + 32 * sub2 + 8 * a + 4 * h);
-            }
-        }
+        // fp8 scales of four entries at a time, read a step or two before they are used
+        f32x4 four[2];
+        auto read_scales = [&](int a, const float *from) {
+            if constexpr (FP8) four[a & 1] = *(const f32x4 *)(from + 8 * a + 4 * (ln >> 5));
+        };
+        read_scales(0, sS[FP8 ? stage : 0][1] + 32 * sub);
         float sum = st.l;
-        __builtin_amdgcn_s_setprio(1);                     // before the other wave's softmax: 330 -> 310 us
+        // the products go before the other wave's softmax (bf16: mixed batch 607 -> 575 us); fp8 waves
+        // also widen codes, which must not wait (64-draft trees 1,154 us with, 962 us without)
+        if constexpr (!FP8) __builtin_amdgcn_s_setprio(1);
         f32x16 s;
 #pragma unroll
         for (int v = 0; v < 16; ++v) s[v] = 0.f;
@@ -1186,12 +1185,14 @@ void attend_long_kernel(AttendArgs A) {
             }
 #pragma unroll
             for (int v = EX * i; v < EX * (i + 1); v += 2) {
+                if (v % 4 == 0 && v < 12) read_scales(v / 4 + 1, sS[FP8 ? stage : 0][1] + 32 * sub);
+                if (v == 14) read_scales(0, sS[FP8 ? stage2 : 0][0] + 32 * sub2);
                 float p0 = __builtin_amdgcn_exp2f(fmaf(now[0][v], A.c, -st.mc));
                 float p1 = __builtin_amdgcn_exp2f(fmaf(now[0][v + 1], A.c, -st.mc));
                 sum += p0;
                 sum += p1;
                 if constexpr (FP8) {                      // a masked entry's scale may be anything
-                    const float y0 = p0 * __uint_as_float(vs4[v / 4][v % 4]), y1 = p1 * __uint_as_float(vs4[v / 4][v % 4 + 1]);
+                    const float y0 = p0 * four[v / 4 & 1][v % 4], y1 = p1 * four[v / 4 & 1][v % 4 + 1];
                     p0 = p0 == 0.f ? 0.f : y0;
                     p1 = p1 == 0.f ? 0.f : y1;
                 }
@@ -1208,12 +1209,13 @@ void attend_long_kernel(AttendArgs A) {
             st.o[x % TL::DT] = mma_bf16(va[x / TL::DT][x % TL::DT], b, st.o[x % TL::DT]);
 #pragma unroll
             for (int v = MX * x; v < MX * (x + 1); ++v) {
-                if constexpr (FP8) s[v] *= __uint_as_float(ks4[v / 4][v % 4]);
+                if (v % 4 == 0 && v < 12) read_scales(v / 4 + 1, sS[FP8 ? stage2 : 0][0] + 32 * sub2);
+                if constexpr (FP8) s[v] *= four[v / 4 & 1][v % 4];
                 mx = fmaxf(mx, s[v]);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_s_setprio(0);
+        if constexpr (!FP8) __builtin_amdgcn_s_setprio(0);
         then[0] = s;
         return mx;
     };

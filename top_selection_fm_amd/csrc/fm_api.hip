@@ -634,10 +634,9 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
 // more 256-column blocks.  The entries of a block are split over S workgroups where that ends
 // sooner by this estimate (us; measured per kernel with head_dim 128): rounds of workgroups over
 // the chip x (tiles a workgroup x time a tile + a workgroup's start and end), and for S > 1 the
-// joining launch and its traffic.  Requests of a batch differ in length, so several rounds of
-// smaller parts even out where the matrix unit is the limit (30 trees of 64 drafts over up to
-// 24,576 entries: 1,156 us whole, 988 us in three parts); a memory-bound kernel's rounds share what
-// an idle CU leaves (30 x 32,768 fp8 entries: 393 us whole, 400 us in two).
+// joining launch and its traffic.  Measured: 16 drafts x 4 heads over 2,000 entries 56 us whole,
+// 20 us in 6 parts, 14 us in 16; 30 x 32,768 fp8 entries 389 us whole, 398 us in 2, 419 us in 6;
+// 30 trees of 64 drafts over up to 24,576 entries 947 us whole, 970 us in 6.
 struct AttendPlan {
     int columns, blocks, splits;
     size_t ml_bytes, o_bytes;
@@ -659,14 +658,13 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     const int64_t tiles = (seen + E - 1) / E;
     const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
     const int slots = p.columns == 128 ? 512 : 256;            // workgroups the chip holds at once
-    const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? (f32 ? 5.8 : 1.7) : (fp8 ? 2.9 : 2.4)) *
+    const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? (f32 ? 5.8 : 1.7) : 2.4) *
                         kv->head_dim / 128.0, ends = 6.0;
     const double part = 8e-6 / 4.0 * a->T * a->n_heads * kv->head_dim;   // a split's sums, written and read, at 4 TB/s
     double best = 0;
     for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, tiles / 2)); ++s) {   // 64: the joining wave's lanes
-        double rounds = (double)((wgs * s + slots - 1) / slots);
-        if (p.columns > 32 && rounds > 1) rounds = std::min(rounds, 0.87 * (double)(wgs * s) / slots + 0.2);
-        const double t = rounds * ((double)((tiles + s - 1) / s) * tile + ends) + (s > 1 ? 5.0 + s * part : 0.0);
+        const double t = (double)((wgs * s + slots - 1) / slots) * ((double)((tiles + s - 1) / s) * tile + ends) +
+                         (s > 1 ? 5.0 + s * part : 0.0);
         if (s == 1 || t < best) {
             best = t;
             p.splits = (int)s;
