@@ -16,12 +16,13 @@
 // fp8 caches the probabilities are rounded to bf16 for the second product (relative 2^-9 each,
 // like the rounding of the output itself), their sum is taken before the rounding.
 //
-// Two kernels share that inner step:
+// The kernels:
 //   attend_split_kernel  few columns (<= 32): the four waves of a workgroup hold the same columns
 //                        and each streams tiles of its own, without barriers; bound by memory.
-//   attend_tile_kernel   many columns: a wave has 32 of its own, and the workgroup's four waves
-//                        share each key/value tile; bound by MFMA and the exponentials.
-// Both can split the entries over several workgroups; attend_merge_kernel joins the parts.
+//   attend_block_kernel  more columns, bf16 and fp8: eight waves of 32 columns share each tile;
+//                        bound by MFMA and the exponentials.
+//   attend_tile_kernel   more columns, float32: four waves; bound by the float32 MFMAs.
+// Each can split the entries over several workgroups; attend_merge_kernel joins the parts.
 //
 // Masks: each lane forms a word of visible entries for a tile; tiles every column sees whole skip
 // the test.  A masked entry's key can hold anything (its score is replaced), and so can its
@@ -879,17 +880,17 @@ __device__ __forceinline__ Place place_of(const AttendArgs &A) {
     return {id % A.splits, A.blocks - 1 - id / A.splits, pair % A.n_kv, pair / A.n_kv};
 }
 
-// ------------------------------------------------------------------ many columns
-// Workgroup (split, block of 128 columns, kv head, request).  The next tile's copy (two LDS
-// stages; fp8: registers) is in flight while a tile is worked on, one barrier a tile.
-template <int FMT, int D>
+// ------------------------------------------------------------------ many columns, float32
+// Workgroup (split, block of 128 columns, kv head, request) of four waves, 32 columns each; the
+// 32-entry tiles are shared.  The next tile's copy (two LDS stages) is in flight while a tile is
+// worked on, one barrier a tile.  Bound by the float32 MFMAs (154 TFLOP/s in a large product).
+template <int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void attend_tile_kernel(AttendArgs A) {
+    constexpr int FMT = KEY_F32;
     using TL = Tile<FMT, D>;
-    constexpr bool FP8 = FMT == KEY_FP8;
     constexpr int NI = TL::BYTES / 4096;                  // copy instructions a wave and tile
     __shared__ __align__(16) uint8_t sK0[TL::BYTES], sV0[TL::BYTES], sK1[TL::BYTES], sV1[TL::BYTES];
-    __shared__ float sS[FP8 ? 2 : 1][2][64];
     __shared__ Special<D> sX[4];
     __shared__ Dest sE[4][32];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
@@ -918,46 +919,32 @@ void attend_tile_kernel(AttendArgs A) {
         }
         return i;
     };
-    CodeRegs<FP8 ? 2 : 1> kc, vc;
     auto issue = [&](uint8_t *kt, uint8_t *vt, int t) {
         const int64_t ofs = tile_at<FMT, D>(A, page, hk, t);
-        if constexpr (FP8) {
-            load_codes<2, 256>(kc, kp + ofs, again(tid));
-            load_codes<2, 256>(vc, vp + ofs, again(tid));
-        } else {
 #pragma unroll
-            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + ofs, kt, NI * w + n);
+        for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, true>(kp + ofs, kt, NI * w + n);
 #pragma unroll
-            for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(vp + ofs, vt, NI * w + n);
-        }
+        for (int n = 0; n < NI; ++n) copy_pieces<FMT, D, false>(vp + ofs, vt, NI * w + n);
     };
-    auto work = [&](const uint8_t *kt, const uint8_t *vt, const float *ks, const float *vs, int t) {
+    auto work = [&](const uint8_t *kt, const uint8_t *vt, int t) {
         constexpr uint64_t full = ~0ull >> (64 - TL::E);
         const uint64_t vis = col.valid ? visible(col, t * TL::E, A.mask_ld) & full : full;
-        if (idle || __ballot(col.valid && vis != 0) == 0) return;
-        const bool masked = __ballot(vis != full) != 0;
-        f32x16 s[TL::SUB];
-        const uint32_t klane = again(key0);
-#pragma unroll
-        for (int sub = 0; sub < TL::SUB; ++sub) s[sub] = scores<FMT, D>(kt, klane, sub, q);
-        soften<FMT, D, TL::SUB>(s, masked, vis, A.c, ks, vs, st);
-        add_values<FMT, D, TL::SUB>(vt, again(value0), s, masked && any_special<FMT, D>(vt), vis, st, sX[w]);
+        if (idle || __builtin_amdgcn_ballot_w64(col.valid && vis != 0) == 0) return;
+        const bool masked = __builtin_amdgcn_ballot_w64(vis != full) != 0;
+        SRegs<1> s;
+        s[0] = scores<FMT, D>(kt, again(key0), 0, q);
+        soften<FMT, D, 1>(s, masked, vis, A.c, nullptr, nullptr, st);
+        add_values<FMT, D, 1>(vt, again(value0), s, masked && any_special<FMT, D>(vt), vis, st, sX[w]);
     };
     int i = seek(t0);
     // tile i is on its way to (kt, vt); after the barrier the other stage is free for the next
-    auto step = [&](uint8_t *kt, uint8_t *vt, uint8_t *kn, uint8_t *vn, int stage) {
+    auto step = [&](uint8_t *kt, uint8_t *vt, uint8_t *kn, uint8_t *vn) {
         const int t = sp.at(i);
-        if constexpr (FP8) {
-            const uint32_t me = again(tid);
-            put_codes<2, 256, true>(kc, kt, sS[stage][0], me, as_is);
-            put_codes<2, 256, false>(vc, vt, sS[stage][1], me, as_is);
-        } else {
-            wait_vm<0>();
-        }
+        wait_vm<0>();
         __syncthreads();
         i = seek(i + 1);
         if (i < t1) issue(kn, vn, sp.at(i));
-        work(kt, vt, sS[FP8 ? stage : 0][0], sS[FP8 ? stage : 0][1], t);
+        work(kt, vt, t);
     };
     if (i < t1) issue(sK0, sV0, sp.at(i));
     col = make_col(A, R, rq.row0, rq.n, rq.len);          // beside the first tile's copy
@@ -965,33 +952,33 @@ void attend_tile_kernel(AttendArgs A) {
     st.clear();
     clear_special(sX[w]);
     while (i < t1) {
-        step(sK0, sV0, sK1, sV1, 0);
+        step(sK0, sV0, sK1, sV1);
         if (i >= t1) break;
-        step(sK1, sV1, sK0, sV0, FP8 ? 1 : 0);
+        step(sK1, sV1, sK0, sV0);
     }
     __syncthreads();
     apply_special<FMT, D>(sX[w], st);
     emit_columns<FMT, D>(A, st, c0 + 32 * w, cols, rq.row0, hk, split, w == 0 ? sK0 : w == 1 ? sV0 : w == 2 ? sK1 : sV1, sE[w]);
 }
 
-// ------------------------------------------------------------------ many columns, long runs
+// ------------------------------------------------------------------ many columns, bf16 and fp8
 // Workgroup (split, block of 256 columns, kv head, request) of eight waves, bf16 and fp8 caches.
 // Each wave keeps the matrix unit busy with its own instructions: while a 32-entry tile's
 // exponentials are formed, the next tile's scores run, and while its values are weighed, the next
 // scores' mask and maximum.  Tiles pass through registers (loaded a tile ahead) into three LDS
 // stages, with one barrier a 64-entry tile: when all waves have met in tile i, tile i + 1 is
 // there and the stage of tile i - 1 is free.
-constexpr int kLongNT = 512;
+constexpr int kBlockNT = 512;
 template <int FMT, int D>
 struct Staged {
     using TL = Tile<FMT, D>;
-    static constexpr int N = TL::BYTES / (16 * kLongNT);   // 16-byte pieces a thread
+    static constexpr int N = TL::BYTES / (16 * kBlockNT);   // 16-byte pieces a thread
     u32x4 k[N], v[N];
     __device__ __forceinline__ void load(const uint8_t *kp, const uint8_t *vp, int tid) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) k[n] = *(const u32x4 *)(kp + 16 * kLongNT * n + 16u * (uint32_t)tid);
+        for (int n = 0; n < N; ++n) k[n] = *(const u32x4 *)(kp + 16 * kBlockNT * n + 16u * (uint32_t)tid);
 #pragma unroll
-        for (int n = 0; n < N; ++n) v[n] = *(const u32x4 *)(vp + 16 * kLongNT * n + 16u * (uint32_t)tid);
+        for (int n = 0; n < N; ++n) v[n] = *(const u32x4 *)(vp + 16 * kBlockNT * n + 16u * (uint32_t)tid);
     }
     // fix(row, piece, values): what is written of a piece of values
     template <class F>
@@ -1001,9 +988,9 @@ struct Staged {
         const int r = t / TL::NP, at = t % TL::NP;
         const uint32_t ko = r * TL::ROW + 16 * (at ^ TL::swz_k(r)), vo = r * TL::ROW + 16 * (at ^ TL::swz_v(r));
 #pragma unroll
-        for (int n = 0; n < N; ++n) *(u32x4 *)(kt + ko + 16 * kLongNT * n) = k[n];
+        for (int n = 0; n < N; ++n) *(u32x4 *)(kt + ko + 16 * kBlockNT * n) = k[n];
 #pragma unroll
-        for (int n = 0; n < N; ++n) *(u32x4 *)(vt + vo + 16 * kLongNT * n) = fix(r + kLongNT / TL::NP * n, at, v[n]);
+        for (int n = 0; n < N; ++n) *(u32x4 *)(vt + vo + 16 * kBlockNT * n) = fix(r + kBlockNT / TL::NP * n, at, v[n]);
     }
 };
 template <>
@@ -1011,23 +998,23 @@ struct Staged<KEY_FP8, kDim> {
     CodeRegs<1> k, v;
     __device__ __forceinline__ void load(const uint8_t *kp, const uint8_t *vp, int tid) {
         const uint32_t t = again(tid);
-        load_codes<1, kLongNT>(k, kp, t);
-        load_codes<1, kLongNT>(v, vp, t);
+        load_codes<1, kBlockNT>(k, kp, t);
+        load_codes<1, kBlockNT>(v, vp, t);
     }
     template <class F>
     __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, float *ks, float *vs, int tid, F fix) const {
         const uint32_t t = again(tid);
-        put_codes<1, kLongNT, true>(k, kt, ks, t, as_is);
-        put_codes<1, kLongNT, false>(v, vt, vs, t, fix);
+        put_codes<1, kBlockNT, true>(k, kt, ks, t, as_is);
+        put_codes<1, kBlockNT, false>(v, vt, vs, t, fix);
     }
 };
 
 template <int FMT, int D>
-__global__ __launch_bounds__(kLongNT) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void attend_long_kernel(AttendArgs A) {
+__global__ __launch_bounds__(kBlockNT) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void attend_block_kernel(AttendArgs A) {
     using TL = Tile<FMT, D>;
     constexpr bool FP8 = FMT == KEY_FP8;
-    constexpr int S = 3, NW = kLongNT / 64;
+    constexpr int S = 3, NW = kBlockNT / 64;
     static_assert(TL::SUB == 2, "two 32-entry tiles a tile");
     __shared__ __align__(16) uint8_t sK[S][TL::BYTES], sV[S][TL::BYTES];
     __shared__ float sS[FP8 ? S : 1][2][64];
@@ -1331,10 +1318,9 @@ template <int FMT, int D>
 hipError_t launch(const AttendArgs &a, hipStream_t s) {
     const unsigned wgs = a.blocks ? (unsigned)placed_workgroups(a.n_kv * a.B, (int64_t)a.splits * a.blocks)
                                   : (unsigned)(a.splits * a.n_kv * a.B);
-    if (a.blocks && a.columns == 256) {
-        if constexpr (FMT != KEY_F32) attend_long_kernel<FMT, D><<<dim3(wgs), kLongNT, 0, s>>>(a);
-    } else if (a.blocks) {
-        attend_tile_kernel<FMT, D><<<dim3(wgs), 256, 0, s>>>(a);
+    if (a.blocks) {
+        if constexpr (FMT == KEY_F32) attend_tile_kernel<D><<<dim3(wgs), 256, 0, s>>>(a);
+        else attend_block_kernel<FMT, D><<<dim3(wgs), kBlockNT, 0, s>>>(a);
     } else {
         attend_split_kernel<FMT, D><<<dim3(wgs), 256, 0, s>>>(a);
     }
@@ -1348,6 +1334,7 @@ hipError_t launch(const AttendArgs &a, hipStream_t s) {
 }  // namespace
 
 int attend_tile_entries(int key_fmt) { return key_fmt == KEY_F32 ? 32 : 64; }
+int attend_block_columns(int key_fmt) { return key_fmt == KEY_F32 ? 128 : 256; }
 
 hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s) {
     if (key_fmt == KEY_F32) return head_dim == 64 ? launch<KEY_F32, 64>(a, s) : launch<KEY_F32, 128>(a, s);

@@ -630,8 +630,12 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
 }
 
 // The kernel and the split of the entries.  Up to 32 columns (rows x heads of a kv head) take the
-// kernel whose waves stream tiles of their own, up to 128 (float32: any number) 128-column blocks,
-// more 256-column blocks.  The entries of a block are split over S workgroups where that ends
+// kernel whose waves stream tiles of their own, more are taken in blocks of 256 (float32: 128).
+// Both sides, on problems of at most 32 columns: 12.6 / 20.1, 13.4 / 15.8, 17.1 / 30.6, 12.4 / 15.2,
+// 36.1 / 41.1, 9.3 / 12.9 us, and within 1 us where a call is hardly longer than its launch.  (A
+// block is never smaller than 256 columns: four-wave blocks of 128 took 51.6 against 30.8 and 29.4
+// against 19.3 us over fp8 and the same +- 1 us over bf16, at 33 to 128 columns.)
+// The entries of a block are split over S workgroups where that ends
 // sooner by this estimate (us; measured per kernel with head_dim 128): rounds of workgroups over
 // the chip x (tiles a workgroup x time a tile + a workgroup's start and end), and for S > 1 the
 // joining launch and its traffic.  Measured: 16 drafts x 4 heads over 2,000 entries 56 us whole,
@@ -648,7 +652,7 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     const bool f32 = kv->key_dtype == FM_F32, fp8 = kv->key_dtype == FM_FP8_E4M3_SCALED132;
     const int64_t cols = (int64_t)a->max_rows * G;
     if (cols > 32) {
-        p.columns = cols > 128 && !f32 ? 256 : 128;
+        p.columns = fm::attend_block_columns(key_fmt(kv->key_dtype));
         p.blocks = (int)((cols + p.columns - 1) / p.columns);
     }
     const int64_t rows = std::min<int64_t>(a->max_rows, p.columns / G + 2);
@@ -658,7 +662,7 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     const int64_t tiles = (seen + E - 1) / E;
     const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
     const int slots = p.columns == 128 ? 512 : 256;            // workgroups the chip holds at once
-    const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? (f32 ? 5.8 : 1.7) : 2.4) *
+    const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? 5.8 : 2.4) *
                         kv->head_dim / 128.0, ends = 6.0;
     const double part = 8e-6 / 4.0 * a->T * a->n_heads * kv->head_dim;   // a split's sums, written and read, at 4 TB/s
     double best = 0;
@@ -711,7 +715,6 @@ fm_status run_attend(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t
     x.n_sink = clamp32(n_sink);
     x.tree_mask = tree_mask;
     x.mask_ld = mask_ld;
-    x.columns = p.columns;
     x.blocks = p.blocks;
     x.splits = p.splits;
     x.part_ml = (float2 *)ws;

@@ -253,13 +253,13 @@ struct AttendArgs {
     int window, n_sink;       // entries back from a row's own (itself included); first entries
     const uint64_t *tree_mask;   // [T, mask_ld] or null
     int64_t mask_ld;
-    int columns;              // columns of a workgroup: 32 (split kernel), 128 (tile) or 256 (long)
-    int blocks;               // such blocks of a problem; 0: split kernel
+    int blocks;               // blocks of attend_block_columns columns; 0: at most 32 columns in all
     int splits;               // parts the entries are split into
     float *part_o;            // [splits, T, n_heads, D]
     float2 *part_ml;          // [splits, T, n_heads]: maximum, sum
 };
 int attend_tile_entries(int key_fmt);
+int attend_block_columns(int key_fmt);
 hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s);
 
 // Query/key norms and rotation, keys and values into the pages (qk.hip).
