@@ -396,7 +396,8 @@ fm_status fm_golden_labels(const float *scores, int64_t ld, int T, int n_layers,
  * bytes); out has q's type and must not overlap q.  (q_dtype, key_dtype): (F32, F32), (BF16, BF16),
  * (BF16, SCALED132).  Device preconditions: q_start ascending and <= T, at most max_rows rows a
  * request, seq_lens[b] <= max_seq_len; rows past max_rows are left as they were, longer lengths
- * are cut.
+ * are cut.  A request of more rows than entries has its first rows (and, of a tree, its first
+ * drafts) before entry 0: such a row has no entry of its own, such a draft is not visible.
  */
 typedef struct {
     const void *q;
@@ -424,10 +425,12 @@ size_t fm_attend_workspace_bytes(const fm_attn_desc *a, const fm_kv_desc *kv, in
  * fm_resident_mask).  out = sum_s softmax(scale q . k_s) v_s; a row that sees nothing gets zeros
  * and lse -inf.  window >= 1 (itself included; max_seq_len or more: plain causal), n_sink >= 0.
  * Accuracy: products accumulate in float32, statistics and sums are float32; over bf16 and fp8
- * caches the probabilities are rounded to bf16 for the product with the values (2^-9 relative
- * each), and the output once.  Masked entries may hold anything, NaN and infinities included; a
- * visible NaN or infinity has the effect IEEE arithmetic gives it, except that a row whose every
- * score is -inf counts as one that sees nothing.  Deterministic.
+ * caches the probabilities are rounded to bf16 for the product with the values (2^-8 relative
+ * each), and the output once; scale q . k_s is expected within float32.  Masked entries may hold
+ * anything, NaN and infinities included.  A visible NaN or infinity has the effect IEEE arithmetic
+ * gives it, with two exceptions: a row whose every score is -inf counts as one that sees nothing,
+ * and where a probability is 0 in float32, an infinite value or scale it weighs may count as any
+ * of itself, NaN and nothing.  Deterministic.
  * ws 256-byte aligned, ws_bytes >= fm_attend_workspace_bytes, contents irrelevant.  T = 0 is a no-op.
  */
 fm_status fm_attend_window(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window,

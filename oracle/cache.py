@@ -31,7 +31,7 @@ def tree_rows(bits: np.ndarray, length: int, window: int, n_sink: int) -> np.nda
     pos = base + bits.sum(1)[:, None].astype(np.int64) - 1
     s = np.arange(length)[None]
     see = (s < base) & (s <= pos) & ((s > pos - window) | (s < n_sink))
-    see[:, base:] = bits
+    see[:, max(base, 0):] = bits[:, max(-base, 0):]         # drafts before entry 0 are not there
     return see
 
 

@@ -97,6 +97,18 @@ def test_attend_workspace():
     assert api.fm_attend_workspace_bytes(good_attn(), kv, 64, 0) == 0        # a page's window: one part
 
 
+def test_attend_launch_limits():
+    """More workgroups than a launch holds are refused; so many requests or rows that the joining
+    launch cannot number them are taken whole."""
+    kv = good_kv(n_pools=2, max_seq_len=100000)
+    kv.B = 1 << 20
+    assert attend_status(good_attn(), kv) == UNSUPPORTED
+    kv.B = 70000
+    assert api.fm_attend_workspace_bytes(good_attn(), kv, 1 << 40, 0) == 0
+    kv.B = 1
+    assert api.fm_attend_workspace_bytes(good_attn(max_rows=1 << 22, T=1 << 22), kv, 1 << 40, 0) == 0
+
+
 def test_attend_tree_refusals():
     kv, a = good_kv(n_pools=2), good_attn(max_rows=65, T=65)
     st = lambda mask, ld: status_of(api.fm_attend_tree, a, kv, mask, ld, 100, 0, None, 0, 0)[0]  # noqa: E731

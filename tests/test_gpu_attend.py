@@ -296,3 +296,47 @@ def test_graph_replays():
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1]), i
+
+
+@pytest.mark.parametrize("kind,ns", [("bf16", [20, 75]), ("bf16", [7, 72]), ("fp8x132", [150, 200]), ("f32", [20, 75])])
+@pytest.mark.parametrize("window", [1 << 40, (1 << 31) - 1, 9])
+def test_more_rows_than_entries(kind, ns, window):
+    """Rows and drafts before entry 0: rows see what the formula leaves, whatever the window."""
+    lens = [3, 70]
+    c = U.Cache(120, lens, 2, 128, kind)
+    q = queries(121, sum(ns), 4, 128, kind)
+    got = U.run_attend(c, q, starts(ns), max(ns), 0.1, window, 1)
+    U.check_attend("rows", c, got, U.attend_oracle(c, q, ns, 0.1, window, 1))
+    bits = [U.tree_bits(np.random.default_rng(b), n) for b, n in enumerate(ns)]
+    words = -(-max(ns) // 64)
+    mask = U.pack_bits([r for x in bits for r in x], words).to(DEV)
+    got = U.run_attend(c, q, starts(ns), max(ns), 0.1, window, 1, mask=mask)
+    U.check_attend("drafts", c, got, U.attend_oracle(c, q, ns, 0.1, window, 1, bits=bits))
+
+
+@pytest.mark.parametrize("kind,H,K,ns", [("bf16", 1024, 1, [1, 2]), ("fp8x132", 1024, 2, [2, 1]),
+                                         ("f32", 1024, 1, [2, 1]), ("bf16", 1024, 1024, [2, 1])])
+def test_most_heads(kind, H, K, ns):
+    """More heads a kv head than a workgroup has columns, and as many kv heads."""
+    c = U.Cache(130, [150, 40], K, 128 if kind == "fp8x132" else 64, kind)
+    q = queries(131, sum(ns), H, c.head_dim, kind)
+    got = U.run_attend(c, q, starts(ns), max(ns), 0.1, 100, 2)
+    U.check_attend("heads", c, got, U.attend_oracle(c, q, ns, 0.1, 100, 2))
+
+
+@pytest.mark.parametrize("kind,ns", [("bf16", [1]), ("bf16", [40]), ("fp8x132", [1]), ("fp8x132", [40]), ("f32", [1]),
+                                     ("f32", [40])])
+def test_long_table_of_unmapped_pages(kind, ns):
+    """The longest lengths there are, all but the first and last pages unmapped."""
+    c = U.Cache(140, [128], 2, 128, kind)
+    L = (1 << 31) - 1
+    cells = (L + 63) // 64
+    small = [int(x) for x in c.table[0, :2]]
+    q = queries(141, ns[0], 4, 128, kind)
+    c.d_table = torch.full((1, cells), -1, dtype=torch.int32, device=DEV)
+    c.d_table[0, 0], c.d_table[0, cells - 1] = small[0], small[1]
+    c.d_lens = torch.tensor([L], dtype=torch.int32, device=DEV)
+    got = U.run_attend(c, q, starts(ns), ns[0], 0.1, 64, 10, max_len=L)
+    # the same entries with one unmapped page between them: the last page ends an entry short
+    c.table, c.lens = torch.tensor([[small[0], -1, small[1]]], dtype=torch.int32), [191]
+    U.check_attend("long", c, got, U.attend_oracle(c, q, ns, 0.1, 64, 10))

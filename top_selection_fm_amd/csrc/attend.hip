@@ -13,7 +13,7 @@
 // second product O^T = V^T P^T wants its B operand, if the entries of a k step are taken in that
 // order.  V^T's A operand comes from LDS through the transposing reads (ds_read_b64_tr_b16): no
 // shuffle and no LDS round trip for P.  Statistics, sums and outputs are float32; for bf16 and
-// fp8 caches the probabilities are rounded to bf16 for the second product (relative 2^-9 each,
+// fp8 caches the probabilities are rounded to bf16 for the second product (relative 2^-8 each,
 // like the rounding of the output itself), their sum is taken before the rounding.
 //
 // The kernels:
@@ -180,12 +180,15 @@ __device__ __forceinline__ Col make_col(const AttendArgs &A, int R, int row0, in
         c.hi = c.base;
     }
     c.hi = max(c.hi, 0);
-    c.lo = max(c.pos - (A.window - 1), 0);
+    c.lo = max(max(c.pos, 0) - (A.window - 1), 0);
     c.sink = min(A.n_sink, c.hi);
     if (c.lo >= c.hi) c.lo = c.hi;
     return c;
 }
 
+template <int E> __device__ __forceinline__ int tiles_of(int entries) {    // entries >= 0, up to 2^31 - 1
+    return (int)(((unsigned)entries + E - 1) / E);
+}
 // Tiles of a workgroup's rows i0 .. i1: the first ones up to the sinks, then from the window on.
 struct Span {
     int first;        // tiles 0 .. first - 1
@@ -199,10 +202,10 @@ __device__ __forceinline__ Span make_span(const AttendArgs &A, int i0, int i1, i
     if (i0 > i1 || hi <= 0) return s;
     // a row of a tree sits at base - 1 or later
     const int p0 = A.tree_mask ? len - n - 1 : len - n + i0;
-    const int lo = max(p0 - (A.window - 1), 0);
-    s.first = (min(A.n_sink, hi) + E - 1) / E;
+    const int lo = max(max(p0, 0) - (A.window - 1), 0);
+    s.first = tiles_of<E>(min(A.n_sink, hi));
     s.from = max(lo / E, s.first);
-    s.count = s.first + max((hi + E - 1) / E - s.from, 0);
+    s.count = s.first + max(tiles_of<E>(hi) - s.from, 0);
     return s;
 }
 
@@ -1060,10 +1063,10 @@ void attend_block_kernel(AttendArgs A) {
     // and their values that are not finite are kept out of LDS (a product with a masked entry's 0
     // would make them NaN): the thread that stages such a value marks the columns that see it.
     const int i0 = c0 / A.G, i1 = (min(c0 + 256, cols) - 1) / A.G, base = rq.len - rq.n;
-    const int last = A.tree_mask ? rq.len : base + i1, from = last - (A.window - 1);   // all see [from, upto)
+    const int last = A.tree_mask ? rq.len : base + i1, from = max(last, 0) - (A.window - 1);   // all see [from, upto)
     const int upto = max(0, A.tree_mask ? base : base + i0 + 1), most = A.tree_mask ? rq.len : base + i1 + 1;
     const int whole0 = min(A.n_sink, upto) / TL::E;        // tiles [0, whole0) and [whole1, whole2) are seen whole
-    const int whole1 = (max(from, 0) + TL::E - 1) / TL::E, whole2 = upto / TL::E;
+    const int whole1 = tiles_of<TL::E>(max(from, 0)), whole2 = upto / TL::E;
     auto put = [&](int s, int t, bool edge) {
         uint8_t *kt = sK[s], *vt = sV[s];
         float *ks = sS[FP8 ? s : 0][0], *vs = sS[FP8 ? s : 0][1];

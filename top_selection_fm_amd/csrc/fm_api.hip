@@ -598,6 +598,7 @@ fm_status check_qk(const fm_qk_desc *d, const fm_kv_desc *kv) {
 }
 
 // ---------------------------------------------------------------- attention
+constexpr int64_t kMostAttendWgs = 1 << 22;       // of up to 512 threads, and place_of's padding: 2^32 threads
 int clamp32(int64_t x) { return (int)std::min<int64_t>(x, INT32_MAX); }
 
 fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
@@ -618,9 +619,9 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     REQUIRE(a->q_ld >= row && a->out_ld >= row && a->q_ld % unit == 0 && a->out_ld % unit == 0,
             FM_ERR_INVALID_ARG, "q_ld = %lld, out_ld = %lld (at least %lld, multiples of 16 bytes)",
             (long long)a->q_ld, (long long)a->out_ld, (long long)row);
-    // columns of a problem and workgroups are counted in 32 bits
+    // columns of a problem and threads of a launch are counted in 32 bits
     REQUIRE((int64_t)a->max_rows * a->n_heads < (1 << 30) &&
-                ((int64_t)a->max_rows * a->n_heads / 128 + a->n_heads) * kv->B < (1 << 25),
+                ((int64_t)a->max_rows * a->n_heads / 128 + a->n_heads) * kv->B < kMostAttendWgs,
             FM_ERR_UNSUPPORTED, "max_rows = %d with %d heads and %d requests", a->max_rows, a->n_heads, kv->B);
     if (a->T == 0 || a->max_rows == 0) return FM_OK;
     REQUIRE(a->q && a->out && a->q_start, FM_ERR_INVALID_ARG, "q / out / q_start NULL");
@@ -665,8 +666,11 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? 5.8 : 2.4) *
                         kv->head_dim / 128.0, ends = 6.0;
     const double part = 8e-6 / 4.0 * a->T * a->n_heads * kv->head_dim;   // a split's sums, written and read, at 4 TB/s
+    // at most 64 parts (the joining wave's lanes), and what the launches' grids hold
+    int64_t most = std::min({(int64_t)64, tiles / 2, kMostAttendWgs / wgs});
+    if (kv->B > 65535 || (int64_t)a->max_rows * a->n_heads >= (1 << 25)) most = 1;
     double best = 0;
-    for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, tiles / 2)); ++s) {   // 64: the joining wave's lanes
+    for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
         const double t = (double)((wgs * s + slots - 1) / slots) * ((double)((tiles + s - 1) / s) * tile + ends) +
                          (s > 1 ? 5.0 + s * part : 0.0);
         if (s == 1 || t < best) {
