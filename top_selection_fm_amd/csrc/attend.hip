@@ -856,31 +856,45 @@ void attend_split_kernel(AttendArgs A) {
     emit<FMT, D, N>(A, d, split, tid % P, o);
 }
 
-// A workgroup's part of the entries, block of columns, kv head and request (b < 0: none).
-// Consecutive workgroups run on the chip's 8 XCDs in turn, each with an L2 of its own.  The blocks of
-// one (request, kv head) read the same tiles, so an XCD takes whole pairs, every eighth one (a
-// batch's requests differ in rows, its heads do not); with fewer than eight pairs, a run of blocks
-// each.  Later blocks see more entries and go first.
+// A workgroup's part of the entries, block of columns, kv head and request .
+// Consecutive workgroups run on the chip's 8 XCDs in turn, each with an L2 of its own: with the kv
+// heads innermost, those of one head share an XCD.  Blocks differ in their tiles, and the host does
+// not know them: the longest go first, so that the short ones even out the end.  Each workgroup
+// ranks the blocks for itself, where there are several requests and few enough blocks.  8 ragged
+// requests over 8,192 entries 580 -> 475 us; even batches and single requests the same +- 1%.
 struct Place {
     int split, blk, hk, b;
 };
-__host__ __device__ __forceinline__ int64_t placed_workgroups(int pairs, int64_t per_pair) {
-    return pairs >= 8 ? 8 * ((pairs + 7) / 8 * per_pair) : pairs * per_pair;
-}
-__device__ __forceinline__ Place place_of(const AttendArgs &A) {
-    const int pairs = A.n_kv * A.B, per_pair = A.splits * A.blocks, x = blockIdx.x % 8, n = blockIdx.x / 8;
-    int pair, id;
-    if (pairs >= 8) {
-        pair = x + 8 * (n / per_pair);
-        id = n % per_pair;
-    } else {
-        const int total = gridDim.x, each = total / 8, rem = total % 8;
-        id = (x < rem ? x * (each + 1) : rem * (each + 1) + (x - rem) * each) + n;
-        pair = id / per_pair;
-        id %= per_pair;
+constexpr int kRanked = 256;
+template <int E, int COLS>
+__device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   // kRanked + 4
+    const int hk = blockIdx.x % A.n_kv, n = blockIdx.x / A.n_kv, split = n % A.splits, rank = n / A.splits;
+    const int items = A.B * A.blocks, tid = threadIdx.x;
+    int it = items - 1 - rank;                            // later blocks see more entries
+    if (A.B > 1 && items <= kRanked) {
+        int own = -1;
+        if (tid < items) {
+            const int b = tid / A.blocks, c0 = (tid - b * A.blocks) * COLS;
+            const Req rq = request(A, b);
+            const int cols = rq.n * A.G;
+            own = 0;
+            if (c0 < cols) own = 1 + make_span<E>(A, c0 / A.G, (min(c0 + COLS, cols) - 1) / A.G, rq.n, rq.len).count;
+        }
+        if (tid < kRanked) ranked[tid] = own;
+        __syncthreads();
+        if (tid < items) {
+            int before = 0;
+            for (int k = 0; k < items; k += 4) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) before += ranked[k + u] > own || (ranked[k + u] == own && k + u < tid);
+            }
+            if (before == rank) ranked[kRanked] = tid;
+        }
+        __syncthreads();
+        it = __builtin_amdgcn_readfirstlane(ranked[kRanked]);
     }
-    if (pair >= pairs) return {0, 0, 0, -1};
-    return {id % A.splits, A.blocks - 1 - id / A.splits, pair % A.n_kv, pair / A.n_kv};
+    const int b = it / A.blocks;
+    return {split, it - b * A.blocks, hk, b};
 }
 
 // ------------------------------------------------------------------ many columns, float32
@@ -896,9 +910,9 @@ void attend_tile_kernel(AttendArgs A) {
     __shared__ __align__(16) uint8_t sK0[TL::BYTES], sV0[TL::BYTES], sK1[TL::BYTES], sV1[TL::BYTES];
     __shared__ Special<D> sX[4];
     __shared__ Dest sE[4][32];
+    __shared__ int sP[kRanked + 4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
-    const Place at = place_of(A);
-    if (at.b < 0) return;
+    const Place at = place_of<TL::E, 128>(A, sP);
     const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;
     const Req rq = request(A, b);
     const int cols = rq.n * A.G, c0 = blk * 128;
@@ -1023,9 +1037,9 @@ void attend_block_kernel(AttendArgs A) {
     __shared__ float sS[FP8 ? S : 1][2][64];
     __shared__ Special<D> sX[NW];
     __shared__ Dest sE[NW][32];
+    __shared__ int sP[kRanked + 4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
-    const Place at = place_of(A);
-    if (at.b < 0) return;
+    const Place at = place_of<TL::E, 256>(A, sP);
     const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;
     const Req rq = request(A, b);
     const int cols = rq.n * A.G, c0 = blk * 256;
@@ -1319,8 +1333,7 @@ __global__ __launch_bounds__(256) void attend_merge_kernel(AttendArgs A) {
 
 template <int FMT, int D>
 hipError_t launch(const AttendArgs &a, hipStream_t s) {
-    const unsigned wgs = a.blocks ? (unsigned)placed_workgroups(a.n_kv * a.B, (int64_t)a.splits * a.blocks)
-                                  : (unsigned)(a.splits * a.n_kv * a.B);
+    const unsigned wgs = (unsigned)((int64_t)a.splits * a.n_kv * a.B * std::max(a.blocks, 1));
     if (a.blocks) {
         if constexpr (FMT == KEY_F32) attend_tile_kernel<D><<<dim3(wgs), 256, 0, s>>>(a);
         else attend_block_kernel<FMT, D><<<dim3(wgs), kBlockNT, 0, s>>>(a);
