@@ -340,3 +340,24 @@ def test_long_table_of_unmapped_pages(kind, ns):
     # the same entries with one unmapped page between them: the last page ends an entry short
     c.table, c.lens = torch.tensor([[small[0], -1, small[1]]], dtype=torch.int32), [191]
     U.check_attend("long", c, got, U.attend_oracle(c, q, ns, 0.1, 64, 10))
+
+
+@pytest.mark.parametrize("kind,D,ns,lens,window", [
+    ("bf16", 64, [200, 1, 0, 77, 150], [1100, 1300, 900, 1090, 200], 1 << 20),
+    ("fp8x132", 128, [200, 1, 0, 77, 150], [1100, 1300, 900, 1090, 200], 1 << 20),
+    ("f32", 64, [100, 1, 0, 77, 50], [700, 800, 600, 90, 60], 1 << 20),
+    ("bf16", 64, [100] * 9, [1030] * 9, 1 << 20),                 # alike: every block of one length but the last ones
+    ("bf16", 64, [24] * 35 + [0, 1], [64 * i + 5 for i in range(37)], 1 << 20),   # trees and windows of one block each
+    ("f32", 64, [20] * 30, [25 * i for i in range(30)], 1 << 20)])
+def test_ragged_batches(kind, D, ns, lens, window):
+    """Enough blocks of unlike lengths that their order matters: each is worked on, once."""
+    H, K = 64, 8
+    c = U.Cache(150, lens, K, D, kind)
+    q = queries(151, sum(ns), H, D, kind)
+    got = U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0)
+    U.check_attend("ragged", c, got, U.attend_oracle(c, q, ns, D ** -0.5, window, 0))
+    if max(ns) <= 64:
+        bits = [U.tree_bits(np.random.default_rng(b), n) for b, n in enumerate(ns)]
+        mask = U.pack_bits([r for x in bits for r in x], 1).to(DEV)
+        got = U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0, mask=mask)
+        U.check_attend("ragged trees", c, got, U.attend_oracle(c, q, ns, D ** -0.5, window, 0, bits=bits))

@@ -856,22 +856,20 @@ void attend_split_kernel(AttendArgs A) {
     emit<FMT, D, N>(A, d, split, tid % P, o);
 }
 
-// A workgroup's part of the entries, block of columns, kv head and request .
-// Consecutive workgroups run on the chip's 8 XCDs in turn, each with an L2 of its own: with the kv
-// heads innermost, those of one head share an XCD.  Blocks differ in their tiles, and the host does
-// not know them: the longest go first, so that the short ones even out the end.  Each workgroup
-// ranks the blocks for itself, where there are several requests and few enough blocks.  8 ragged
-// requests over 8,192 entries 580 -> 475 us; even batches and single requests the same +- 1%.
+// A workgroup's part of the entries, block of columns, kv head and request.  Consecutive workgroups
+// run on the chip's 8 XCDs in turn, each with an L2 of its own: with the kv heads innermost, those
+// of one head share an XCD.  Blocks differ in their tiles, which the host does not know; where that
+// matters (ranked) each workgroup ranks them for itself, and the longest go first, so that the
+// short ones even out the end.
 struct Place {
     int split, blk, hk, b;
 };
-constexpr int kRanked = 256;
 template <int E, int COLS>
-__device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   // kRanked + 4
+__device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   // kAttendRanked + 4
     const int hk = blockIdx.x % A.n_kv, n = blockIdx.x / A.n_kv, split = n % A.splits, rank = n / A.splits;
     const int items = A.B * A.blocks, tid = threadIdx.x;
     int it = items - 1 - rank;                            // later blocks see more entries
-    if (A.B > 1 && items <= kRanked) {
+    if (A.ranked) {
         int own = -1;
         if (tid < items) {
             const int b = tid / A.blocks, c0 = (tid - b * A.blocks) * COLS;
@@ -880,18 +878,19 @@ __device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   
             own = 0;
             if (c0 < cols) own = 1 + make_span<E>(A, c0 / A.G, (min(c0 + COLS, cols) - 1) / A.G, rq.n, rq.len).count;
         }
-        if (tid < kRanked) ranked[tid] = own;
+        if (tid < kAttendRanked) ranked[tid] = own;
         __syncthreads();
         if (tid < items) {
             int before = 0;
             for (int k = 0; k < items; k += 4) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) before += ranked[k + u] > own || (ranked[k + u] == own && k + u < tid);
+                const int4 x = *(const int4 *)(ranked + k);
+                before += (x.x > own || (x.x == own && k < tid)) + (x.y > own || (x.y == own && k + 1 < tid)) +
+                          (x.z > own || (x.z == own && k + 2 < tid)) + (x.w > own || (x.w == own && k + 3 < tid));
             }
-            if (before == rank) ranked[kRanked] = tid;
+            if (before == rank) ranked[kAttendRanked] = tid;
         }
         __syncthreads();
-        it = __builtin_amdgcn_readfirstlane(ranked[kRanked]);
+        it = __builtin_amdgcn_readfirstlane(ranked[kAttendRanked]);
     }
     const int b = it / A.blocks;
     return {split, it - b * A.blocks, hk, b};
@@ -910,7 +909,7 @@ void attend_tile_kernel(AttendArgs A) {
     __shared__ __align__(16) uint8_t sK0[TL::BYTES], sV0[TL::BYTES], sK1[TL::BYTES], sV1[TL::BYTES];
     __shared__ Special<D> sX[4];
     __shared__ Dest sE[4][32];
-    __shared__ int sP[kRanked + 4];
+    __shared__ __align__(16) int sP[kAttendRanked + 4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
     const Place at = place_of<TL::E, 128>(A, sP);
     const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;
@@ -1037,7 +1036,7 @@ void attend_block_kernel(AttendArgs A) {
     __shared__ float sS[FP8 ? S : 1][2][64];
     __shared__ Special<D> sX[NW];
     __shared__ Dest sE[NW][32];
-    __shared__ int sP[kRanked + 4];
+    __shared__ __align__(16) int sP[kAttendRanked + 4];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), ln = __lane_id(), j = ln & 31;
     const Place at = place_of<TL::E, 256>(A, sP);
     const int split = at.split, blk = at.blk, hk = at.hk, b = at.b;

@@ -636,18 +636,19 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
 // 36.1 / 41.1, 9.3 / 12.9 us, and within 1 us where a call is hardly longer than its launch.  (A
 // block is never smaller than 256 columns: four-wave blocks of 128 took 51.6 against 30.8 and 29.4
 // against 19.3 us over fp8 and the same +- 1 us over bf16, at 33 to 128 columns.)
-// The entries of a block are split over S workgroups where that ends
-// sooner by this estimate (us; measured per kernel with head_dim 128): rounds of workgroups over
-// the chip x (tiles a workgroup x time a tile + a workgroup's start and end), and for S > 1 the
-// joining launch and its traffic.  Measured: 16 drafts x 4 heads over 2,000 entries 56 us whole,
-// 20 us in 6 parts, 14 us in 16; 30 x 32,768 fp8 entries 389 us whole, 398 us in 2, 419 us in 6;
-// 30 trees of 64 drafts over up to 24,576 entries 947 us whole, 970 us in 6.
+// The entries of a block are split over S workgroups where that ends sooner by this estimate (us;
+// measured per kernel with head_dim 128): rounds of workgroups over the chip x (tiles a workgroup x
+// time a tile + a workgroup's start and end), and for S > 1 the joining launch and its traffic.
+// Measured: 16 drafts x 4 heads over 2,000 entries 48 us whole, 21 us in 4 parts, 14 us in 16; 8
+// ragged requests over 8,192 entries 454 us whole, 544 us in 2; 30 x 32,768 fp8 entries 389 us
+// whole, 398 us in 2, 419 us in 6; 30 trees of 64 drafts over up to 24,576 entries 951 us whole,
+// 922 us in 2 (by the estimate the same; their lengths, which it does not know, differ by a third).
 struct AttendPlan {
-    int columns, blocks, splits;
+    int columns, blocks, splits, ranked;
     size_t ml_bytes, o_bytes;
 };
 AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t window, int64_t n_sink) {
-    AttendPlan p{32, 0, 1, 0, 0};
+    AttendPlan p{32, 0, 1, 0, 0, 0};
     if (a->T == 0 || a->max_rows == 0) return p;
     const int G = a->n_heads / a->n_kv_heads;
     const bool f32 = kv->key_dtype == FM_F32, fp8 = kv->key_dtype == FM_FP8_E4M3_SCALED132;
@@ -661,23 +662,35 @@ AttendPlan attend_plan(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
     const int64_t seen = std::min<int64_t>(std::min<int64_t>(window, kv->max_seq_len) + rows +
                                                std::min<int64_t>(n_sink, kv->max_seq_len), kv->max_seq_len);
     const int64_t tiles = (seen + E - 1) / E;
-    const int64_t wgs = (int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1);
+    // blocks that hold rows: T rows in all, and a request's last block may be partly filled
+    const int64_t blocks = std::min<int64_t>((int64_t)kv->B * std::max(p.blocks, 1),
+                                             (int64_t)a->T * G / p.columns + kv->B);
+    const int64_t wgs = blocks * a->n_kv_heads;
+    const bool even = (int64_t)kv->B * a->max_rows <= a->T;   // else short blocks fill the last round
     const int slots = p.columns == 128 ? 512 : 256;            // workgroups the chip holds at once
     const double tile = (p.columns == 32 ? (fp8 ? 0.8 : 1.5) : p.columns == 128 ? 5.8 : 2.4) *
                         kv->head_dim / 128.0, ends = 6.0;
     const double part = 8e-6 / 4.0 * a->T * a->n_heads * kv->head_dim;   // a split's sums, written and read, at 4 TB/s
     // at most 64 parts (the joining wave's lanes), and what the launches' grids hold
-    int64_t most = std::min({(int64_t)64, tiles / 2, kMostAttendWgs / wgs});
+    int64_t most = std::min({(int64_t)64, tiles / 2,
+                             kMostAttendWgs / ((int64_t)kv->B * a->n_kv_heads * std::max(p.blocks, 1))});
     if (kv->B > 65535 || (int64_t)a->max_rows * a->n_heads >= (1 << 25)) most = 1;
     double best = 0;
     for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
-        const double t = (double)((wgs * s + slots - 1) / slots) * ((double)((tiles + s - 1) / s) * tile + ends) +
+        const double full = (double)(wgs * s) / slots, whole = ceil(full);
+        const double rounds = even || full <= 1 ? whole : (full + whole) / 2;
+        const double t = rounds * ((double)((tiles + s - 1) / s) * tile + ends) +
                          (s > 1 ? 5.0 + s * part : 0.0);
         if (s == 1 || t < best) {
             best = t;
             p.splits = (int)s;
         }
     }
+    // The longest blocks first where blocks differ, are long enough to pay for each workgroup's
+    // ranking of them (2 us) and do not all run at once.  Both sides: 8 ragged requests over 8,192
+    // entries 580 / 470 us; 2 x 2,190 rows under a window of 58 60 / 70 us.
+    const int64_t items = (int64_t)kv->B * p.blocks;
+    p.ranked = kv->B > 1 && items <= fm::kAttendRanked && items * a->n_kv_heads * p.splits > 256 && tiles >= 16 * p.splits;
     if (p.splits > 1) {
         const size_t parts = (size_t)p.splits * a->T * a->n_heads;
         p.ml_bytes = fm::align_up(parts * sizeof(float2), 256);
@@ -721,6 +734,7 @@ fm_status run_attend(const fm_attn_desc *a, const fm_kv_desc *kv, const uint64_t
     x.mask_ld = mask_ld;
     x.blocks = p.blocks;
     x.splits = p.splits;
+    x.ranked = p.ranked;
     x.part_ml = (float2 *)ws;
     x.part_o = (float *)((uint8_t *)ws + p.ml_bytes);
     CHECK(launched(fm::launch_attend(x, key_fmt(kv->key_dtype), kv->head_dim, (hipStream_t)stream), "attention"));

@@ -255,9 +255,11 @@ struct AttendArgs {
     int64_t mask_ld;
     int blocks;               // blocks of attend_block_columns columns; 0: at most 32 columns in all
     int splits;               // parts the entries are split into
+    int ranked;               // blocks go by their tiles, most first (B blocks <= kAttendRanked)
     float *part_o;            // [splits, T, n_heads, D]
     float2 *part_ml;          // [splits, T, n_heads]: maximum, sum
 };
+constexpr int kAttendRanked = 256;
 int attend_tile_entries(int key_fmt);
 int attend_block_columns(int key_fmt);
 hipError_t launch_attend(const AttendArgs &a, int key_fmt, int head_dim, hipStream_t s);
