@@ -361,3 +361,29 @@ def test_ragged_batches(kind, D, ns, lens, window):
         mask = U.pack_bits([r for x in bits for r in x], 1).to(DEV)
         got = U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0, mask=mask)
         U.check_attend("ragged trees", c, got, U.attend_oracle(c, q, ns, D ** -0.5, window, 0, bits=bits))
+
+
+@pytest.mark.parametrize("ns", [[1, 2], [70, 40]])
+def test_wild_scales_seen_by_some_rows(ns):
+    """fp8 values whose scale is an infinity or NaN, and codes that are NaN, reach the rows that see
+    them alone, each as code times scale is in IEEE arithmetic."""
+    lens, window = [200, 100], 30
+    c = U.Cache(160, lens, 2, 128, "fp8x132")
+    q = queries(161, sum(ns), 4, 128, "bf16")
+    for b in range(2):
+        for h, (back, scale) in enumerate(((1, float("inf")), (29, float("-inf")))):
+            s = lens[b] - back
+            row = c.pools[1][int(c.table[b, s // 64]), h, s % 64]
+            row[128:] = torch.tensor([scale]).view(torch.uint8)
+            row[5] = 0                                               # 0 inf
+        s = lens[b] - 31
+        c.pools[1][int(c.table[b, s // 64]), 0, s % 64, 7] = 0x7f
+        s = lens[b] - 2
+        c.pools[1][int(c.table[b, s // 64]), 1, s % 64, 128:] = torch.tensor([float("nan")]).view(torch.uint8)
+    c.upload()
+    out, lse = U.run_attend(c, q, starts(ns), max(ns), 0.1, window, 0)
+    want = U.attend_oracle(c, q, ns, 0.1, window, 0)
+    got, bad = out.double().cpu().numpy(), ~np.isfinite(want[0])
+    assert np.isposinf(want[0]).any() and np.isneginf(want[0]).any() and np.isnan(want[0]).any()
+    assert np.array_equal(got[bad], want[0][bad], equal_nan=True) and np.isfinite(got[~bad]).all()
+    assert bool(torch.isfinite(lse).all())

@@ -572,7 +572,7 @@ __device__ __forceinline__ void copy_pieces(const uint8_t *src, uint8_t *dst, in
     __builtin_amdgcn_global_load_lds((const void *)(src + 1024 * n + ofs), (lds_void *)(dst + 1024 * n), 16, 0, 0);
 }
 
-constexpr auto as_is = [](int, int, u32x4 y) { return y; };   // a piece as it was loaded
+constexpr auto as_is = [](int, int, u32x4 y, float) { return y; };   // a piece as it was loaded
 
 // fp8 tiles pass through registers: 16 codes a piece, widened exactly to bf16.
 template <int N>
@@ -580,14 +580,17 @@ struct CodeRegs {
     u32x4 x[N];
     float scale;
 };
-template <int N, int NT>   // N pieces a thread, NT threads
+// N pieces a thread, NT threads; scales are loaded by the first 64 threads or (OWN, N = 1) by each
+// for its piece.
+template <int N, int NT, bool OWN = false>
 __device__ __forceinline__ void load_codes(CodeRegs<N> &c, const uint8_t *src, uint32_t tid) {
     const uint32_t lane = (tid >> 3) * kRowFp8 + 16 * (tid & 7);
 #pragma unroll
     for (int i = 0; i < N; ++i) c.x[i] = *(const u32x4_u *)(src + lane + (NT / 8) * kRowFp8 * i);
-    if (tid < 64) c.scale = *(const float *)(src + tid * kRowFp8 + kDim);
+    if constexpr (OWN) c.scale = *(const float *)(src + (tid >> 3) * kRowFp8 + kDim);
+    else if (tid < 64) c.scale = *(const float *)(src + tid * kRowFp8 + kDim);
 }
-template <int N, int NT, bool KEYS, class F>
+template <int N, int NT, bool KEYS, bool OWN = false, class F>
 __device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, float *scales, uint32_t tid, F fix) {
     using TL = Tile<KEY_FP8, kDim>;
     auto swz = [](int r) { return KEYS ? TL::swz_k(r) : TL::swz_v(r); };
@@ -604,9 +607,13 @@ __device__ __forceinline__ void put_codes(const CodeRegs<N> &c, uint8_t *dst, fl
                 y[2 * w + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(d, 1.0f, true));
             }
             *(u32x4 *)(dst + (lane ^ (uint32_t)(16 * (o ^ swz(NT / 8 * i)))) + NT / 8 * i * TL::ROW) =
-                fix(r + NT / 8 * i, 2 * (tid & 7) + o, y);
+                fix(r + NT / 8 * i, 2 * (tid & 7) + o, y, c.scale);
         }
-    if (tid < 64) scales[tid] = c.scale;
+    if constexpr (OWN) {
+        if ((tid & 7) == 0) scales[r] = c.scale;
+    } else {
+        if (tid < 64) scales[tid] = c.scale;
+    }
 }
 
 // The page of tile `t` of request b, or -1 where it is not mapped.
@@ -899,7 +906,9 @@ __device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   
 // ------------------------------------------------------------------ many columns, float32
 // Workgroup (split, block of 128 columns, kv head, request) of four waves, 32 columns each; the
 // 32-entry tiles are shared.  The next tile's copy (two LDS stages) is in flight while a tile is
-// worked on, one barrier a tile.  Bound by the float32 MFMAs (154 TFLOP/s in a large product).
+// worked on, one barrier a tile.  Bound by the float32 MFMAs (154 TFLOP/s in a large product) and,
+// with one workgroup a CU, by the latency from scores to sums: 5.3 to 5.8 us a tile of 128 x 128
+// either way.  3 requests of up to 333 rows x 12 heads of 64 dims: 26 us and 4 us to join.
 template <int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void attend_tile_kernel(AttendArgs A) {
@@ -983,7 +992,16 @@ void attend_tile_kernel(AttendArgs A) {
 // exponentials are formed, the next tile's scores run, and while its values are weighed, the next
 // scores' mask and maximum.  Tiles pass through registers (loaded a tile ahead) into three LDS
 // stages, with one barrier a 64-entry tile: when all waves have met in tile i, tile i + 1 is
-// there and the stage of tile i - 1 is free.
+// there and the stage of tile i - 1 is free.  (Copied straight into LDS they cost 3 to 5% more:
+// prefill 287 / 296 us, ragged batch 460 / 481 us; the swizzle is then the source address's, a lane.)
+//
+// Bound by instruction issue: at 256 columns a workgroup and one workgroup a CU the MFMAs are busy
+// 40% of the cycles at 1.9 GHz, the exponentials, maxima and packing beside them fill most of the
+// rest.  4,096 rows x 32 heads under a window of 2,048: 290 us, 949 TFLOP/s (a large bf16 product:
+// 1,236); without the staging 278, the barrier 262, the second product 277, the first 322 of 315 us
+// in a timing copy.  8 ragged requests over 8,192 entries 460 us, 900 TFLOP/s.  fp8 also widens
+// codes and multiplies two scales: 30 trees of 64 drafts over up to 24,576 entries 900 us, 744
+// TFLOP/s, on 240 of 256 CUs.
 constexpr int kBlockNT = 512;
 template <int FMT, int D>
 struct Staged {
@@ -1006,7 +1024,8 @@ struct Staged {
 #pragma unroll
         for (int n = 0; n < N; ++n) *(u32x4 *)(kt + ko + 16 * kBlockNT * n) = k[n];
 #pragma unroll
-        for (int n = 0; n < N; ++n) *(u32x4 *)(vt + vo + 16 * kBlockNT * n) = fix(r + kBlockNT / TL::NP * n, at, v[n]);
+        for (int n = 0; n < N; ++n) *(u32x4 *)(vt + vo + 16 * kBlockNT * n) =
+            fix(r + kBlockNT / TL::NP * n, at, v[n], 1.f);
     }
 };
 template <>
@@ -1015,13 +1034,13 @@ struct Staged<KEY_FP8, kDim> {
     __device__ __forceinline__ void load(const uint8_t *kp, const uint8_t *vp, int tid) {
         const uint32_t t = again(tid);
         load_codes<1, kBlockNT>(k, kp, t);
-        load_codes<1, kBlockNT>(v, vp, t);
+        load_codes<1, kBlockNT, true>(v, vp, t);
     }
     template <class F>
     __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, float *ks, float *vs, int tid, F fix) const {
         const uint32_t t = again(tid);
         put_codes<1, kBlockNT, true>(k, kt, ks, t, as_is);
-        put_codes<1, kBlockNT, false>(v, vt, vs, t, fix);
+        put_codes<1, kBlockNT, false, true>(v, vt, vs, t, fix);
     }
 };
 
@@ -1087,8 +1106,9 @@ void attend_block_kernel(AttendArgs A) {
             in.put(kt, vt, ks, vs, tid, as_is);
             return;
         }
-        in.put(kt, vt, ks, vs, tid, [&](int r, int piece, u32x4 y) {
-            uint32_t bad = 0;
+        in.put(kt, vt, ks, vs, tid, [&](int r, int piece, u32x4 y, float scale) {
+            const bool wild = !(fabsf(scale) < __builtin_inff());
+            uint32_t bad = wild;
 #pragma unroll
             for (int d = 0; d < 4; ++d) bad |= ((y[d] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
             if (bad == 0) return y;
@@ -1102,16 +1122,20 @@ void attend_block_kernel(AttendArgs A) {
 #pragma unroll 1
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t word = e < 2 ? y[0] : e < 4 ? y[1] : e < 6 ? y[2] : y[3];
-                    const uint32_t f = e & 1 ? word & 0xffff0000u : word << 16;
+                    uint32_t f = e & 1 ? word & 0xffff0000u : word << 16;
+                    if constexpr (FP8) f = __float_as_uint(__uint_as_float(f) * scale);
                     if ((f & 0x7f800000u) != 0x7f800000u) continue;
                     uint32_t *to = f & 0x007fffffu ? x.nan[c % 32] : f >> 31 ? x.down[c % 32] : x.up[c % 32];
                     atomicOr(&to[piece / 4], 1u << (8 * (piece % 4) + e));
                 }
             }
 #pragma unroll
-            for (int d = 0; d < 4; ++d) y[d] = finite_only<false>(y[d]);
+            for (int d = 0; d < 4; ++d) y[d] = wild ? 0u : finite_only<false>(y[d]);
             return y;
         });
+        if constexpr (FP8) {                               // those values are zeros: any scale will do
+            if ((tid & 7) == 0 && !(fabsf(in.v.scale) < __builtin_inff())) vs[tid >> 3] = 0.f;
+        }
     };
 
     // the scores of the 32-entry tile being worked on and of the next; the mask of their tile
@@ -1194,10 +1218,9 @@ void attend_block_kernel(AttendArgs A) {
                 float p1 = __builtin_amdgcn_exp2f(fmaf(now[0][v + 1], A.c, -st.mc));
                 sum += p0;
                 sum += p1;
-                if constexpr (FP8) {                      // a masked entry's scale may be anything
-                    const float y0 = p0 * four[v / 4 & 1][v % 4], y1 = p1 * four[v / 4 & 1][v % 4 + 1];
-                    p0 = p0 == 0.f ? 0.f : y0;
-                    p1 = p1 == 0.f ? 0.f : y1;
+                if constexpr (FP8) {
+                    p0 *= four[v / 4 & 1][v % 4];
+                    p1 *= four[v / 4 & 1][v % 4 + 1];
                 }
                 pk[v / 8][v % 8 / 4][v % 4 / 2] = pack_bf16(p0, p1);
             }
