@@ -103,26 +103,37 @@ __device__ __forceinline__ int team_size(int n) {
     return t;
 }
 
-// Whether entry i of a compaction may be carried out, as far as thread `lane` of `lanes` checks
-// it: the kept entries ascending within [start, len), and every page that receives or gives a
-// moved entry mapped, the receiving ones held by this request alone.
-__device__ __forceinline__ bool keep_is_good(const CacheArgs &A, int i, int r, int len, int lane, int lanes) {
-    const int start = A.start[i], k = A.n_keep[i];
-    if (start < 0 || start > len || k < 0 || k > A.keep_ld || k > len - start) return false;
+// Entry i of a compaction: where it starts, how many entries it keeps, and of those the thread's
+// first and the one before, read without waiting for each other.
+struct Kept {
+    int start, k, s, prev;
+};
+__device__ __forceinline__ Kept read_kept(const CacheArgs &A, int i, int lane) {
+    const int32_t *keep = A.keep + (int64_t)i * A.keep_ld;
+    return {A.start[i], A.n_keep[i], lane < A.keep_ld ? keep[lane] : -1, lane && lane < A.keep_ld ? keep[lane - 1] : -1};
+}
+// Whether it may be carried out, as far as thread `lane` of `lanes` checks it: the kept entries
+// ascending within [start, len), and every page that receives or gives a moved entry mapped, the
+// receiving ones held by this request alone.  The pages are read while len is on its way.
+__device__ __forceinline__ bool keep_is_good(const CacheArgs &A, int i, int r, int len, const Kept &e, int lane, int lanes) {
     const int32_t *keep = A.keep + (int64_t)i * A.keep_ld;
     const int32_t *row = A.block_table + (int64_t)r * A.bt_ld;
-    bool good = true;
-    for (int j = lane; j < k; j += lanes) {
-        const int s = keep[j], prev = j ? keep[j - 1] : start - 1;
-        if (s <= prev || s < start || s >= len) {
+    const int64_t cells = A.bt_ld * kPage;
+    bool good = e.start >= 0 && e.k >= 0 && e.k <= A.keep_ld;
+    const int k = good ? e.k : 0;
+    for (int j = lane; j < k && good; j += lanes) {
+        const int s = j == lane ? e.s : keep[j], prev = j == 0 ? e.start - 1 : j == lane ? e.prev : keep[j - 1];
+        const int64_t d = (int64_t)e.start + j;
+        if (s <= prev || s < d || s >= cells) {            // so d < cells too
             good = false;
-            break;
+        } else if (s != d) {
+            const int from = row[s / kPage], to = row[d / kPage];
+            const bool live = to >= 0 && to < A.n_phys;
+            good = from >= 0 && from < A.n_phys && live && A.ref[live ? to : 0] == 1;
         }
-        if (s == start + j) continue;
-        const int from = row[s / kPage], to = row[(start + j) / kPage];
-        if (from < 0 || from >= A.n_phys || to < 0 || to >= A.n_phys || A.ref[to] != 1) good = false;
+        good = good && s < len;
     }
-    return good;
+    return good && e.start <= len && e.k <= len - e.start;
 }
 
 // Requests cut to a new length: freeing (COMPACT false; new_len[i], or 0) and the end of a
@@ -140,9 +151,11 @@ __global__ __launch_bounds__(kPlanNT) void cache_release_kernel(CacheArgs A) {
     // entry i's request, its length and where it is cut; with an entry a team they stay in
     // registers from the verdict to the release
     int r = -1, len = 0, cut = 0;
+    Kept kept = {};
     auto look = [&](int i) {
         r = A.req[i];
-        cut = COMPACT ? A.start[i] + A.n_keep[i] : A.new_len ? A.new_len[i] : 0;
+        if constexpr (COMPACT) kept = read_kept(A, i, lane);
+        cut = COMPACT ? kept.start + kept.k : A.new_len ? A.new_len[i] : 0;
         len = r >= 0 && r < A.B ? length_of(A, r) : -1;
     };
     if (first < A.n) look(first);
@@ -154,7 +167,7 @@ __global__ __launch_bounds__(kPlanNT) void cache_release_kernel(CacheArgs A) {
         if (i != first) look(i);
         bool good = len >= 0 && claims[r] == i;
         if (good) {
-            if constexpr (COMPACT) good = keep_is_good(A, i, r, len, lane, team);
+            if constexpr (COMPACT) good = keep_is_good(A, i, r, len, kept, lane, team);
             else good = cut >= 0 && cut <= len;
         }
         if (!good) bad[i] = 1;
@@ -358,6 +371,7 @@ __global__ __launch_bounds__(256) void cache_move_kernel(CacheArgs A) {
     __shared__ int bad, moved;
     const int head = blockIdx.x, i = blockIdx.y, pool = blockIdx.z, tid = threadIdx.x;
     if (head >= A.heads[pool]) return;
+    const Kept kept = read_kept(A, i, tid);
     const int r = A.req[i];
     if (r < 0 || r >= A.B) return;
     if (tid == 0) bad = 0, moved = INT32_MAX;
@@ -365,15 +379,15 @@ __global__ __launch_bounds__(256) void cache_move_kernel(CacheArgs A) {
     const int len = length_of(A, r);
     bool good = true;
     for (int j = tid; j < i; j += 256) good = good && A.req[j] != r;
-    good = good && keep_is_good(A, i, r, len, tid, 256);
+    good = keep_is_good(A, i, r, len, kept, tid, 256) && good;
     if (!good) bad = 1;
     __syncthreads();
     if (bad) return;
     const int32_t *keep = A.keep + (int64_t)i * A.keep_ld;
-    const int start = A.start[i], k = A.n_keep[i];
+    const int start = kept.start, k = kept.k;
     // entries from the first that moves on all move
     for (int j = tid; j < k; j += 256)
-        if (keep[j] != start + j) {
+        if ((j == tid ? kept.s : keep[j]) != start + j) {
             atomicMin(&moved, j);
             break;
         }
