@@ -88,6 +88,9 @@ __device__ __forceinline__ uint32_t again(uint32_t x) {
     return x;
 }
 
+// A value that is formed here, not where it is used.
+__device__ __forceinline__ void here(float &x) { asm volatile("" : "+v"(x)); }
+
 template <int N> __device__ __forceinline__ void wait_vm() {     // s_waitcnt vmcnt(N), others left alone
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
     __builtin_amdgcn_sched_barrier(0);
@@ -1226,6 +1229,7 @@ void attend_block_kernel(AttendArgs A) {
                 }
                 pk[v / 8][v % 8 / 4][v % 4 / 2] = pack_bf16(p0, p1);
             }
+            here(sum);
             __builtin_amdgcn_sched_barrier(0);
         }
         st.l = sum;
@@ -1241,6 +1245,7 @@ void attend_block_kernel(AttendArgs A) {
                 if constexpr (FP8) s[v] *= four[v / 4 & 1][v % 4];
                 mx = fmaxf(mx, s[v]);
             }
+            here(mx);
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (!FP8) __builtin_amdgcn_s_setprio(0);
