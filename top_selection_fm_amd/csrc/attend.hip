@@ -1000,13 +1000,13 @@ void attend_tile_kernel(AttendArgs A) {
 // there and the stage of tile i - 1 is free.  (Copied straight into LDS they cost 3 to 5% more:
 // prefill 287 / 296 us, ragged batch 460 / 481 us; the swizzle is then the source address's, a lane.)
 //
-// Bound by instruction issue: at 256 columns a workgroup and one workgroup a CU the MFMAs are busy
-// 40% of the cycles at 1.9 GHz, the exponentials, maxima and packing beside them fill most of the
-// rest.  4,096 rows x 32 heads under a window of 2,048: 290 us, 949 TFLOP/s (a large bf16 product:
-// 1,236); without the staging 278, the barrier 262, the second product 277, the first 322 of 315 us
-// in a timing copy.  8 ragged requests over 8,192 entries 460 us, 900 TFLOP/s.  fp8 also widens
-// codes and multiplies two scales: 30 trees of 64 drafts over up to 24,576 entries 900 us, 744
-// TFLOP/s, on 240 of 256 CUs.
+// Bound by instruction issue and by the clock under this load (1.9 GHz; the same prefill over zeros
+// takes 258 us instead of 296): the MFMAs are busy 41% of the cycles and the vector units 43%, a
+// third of the former beside the latter; the rest is the maximum's lane swap and branch, the
+// barrier (without it, in a timing copy, 262 of 315 us) and waits for LDS.  4,096 rows x 32 heads
+// under a window: 290 us, 949 TFLOP/s (a large bf16 product: 1,236).  8 ragged requests over 8,192
+// entries 455 us, 910 TFLOP/s.  fp8 also widens codes and multiplies two scales: 30 trees of 64
+// drafts over up to 24,576 entries 880 us, 760 TFLOP/s, on 240 of 256 CUs.
 constexpr int kBlockNT = 512;
 template <int FMT, int D>
 struct Staged {
@@ -1085,9 +1085,15 @@ void attend_block_kernel(AttendArgs A) {
     const int64_t head = (int64_t)hk * kPage * row, step = (int64_t)A.n_kv * kPage * row;
     const uint8_t *kp = (const uint8_t *)A.k + head, *vp = (const uint8_t *)A.v + head;
     Staged<FMT, D> in;
+    // a lane has the page of a tile: 64 at once, so that no tile waits for the table
+    int first = t0, pages = t0 + ln < t1 ? page_of<FMT, D>(A, b, sp.at(t0 + ln)) : -1;
     auto fetch = [&](int i) {
         for (; i < t1; ++i) {
-            const int page = __builtin_amdgcn_readfirstlane(page_of<FMT, D>(A, b, sp.at(i)));
+            if (i - first >= 64) {
+                first = i;
+                pages = i + ln < t1 ? page_of<FMT, D>(A, b, sp.at(i + ln)) : -1;
+            }
+            const int page = __builtin_amdgcn_readlane(pages, i - first);
             if (page < 0) continue;
             const int64_t at = page * step;
             in.load(kp + at, vp + at, tid);
@@ -1163,9 +1169,8 @@ void attend_block_kernel(AttendArgs A) {
     };
     // The exponentials of one 32-entry tile beside the scores of the next, then its values; returns
     // the scores' maximum.  Written in the order it is to run in, a matrix instruction and what
-    // fits beside it at a time: the values' reads and two entries' exponentials with each step of the
-    // first product, the scores' scales and maximum with the second.  The keys are read before the
-    // step that uses them (read_keys), behind the maximum's lane swap and branch.
+    // fits beside it at a time.  The keys are read before the step that uses them (read_keys), behind
+    // the maximum's lane swap and branch.
     uint32_t ko[TL::QR], vo[TL::DT];                      // the lane's reads in the current stages
 #pragma unroll
     for (int i = 0; i < TL::QR; ++i) ko[i] = key_lane<FMT, D>() ^ (uint32_t)(32 * i);
@@ -1187,8 +1192,8 @@ void attend_block_kernel(AttendArgs A) {
     };
     auto advance = [&](SRegs<1> &now, int stage, int sub, SRegs<1> &then, int stage2, int sub2) {
         const uint8_t *vt = sV[0] + 32 * sub * TL::ROW;
-        constexpr int QR = TL::QR, PV = 2 * TL::DT;       // matrix instructions of each product
-        constexpr int EX = 16 / QR;                       // entries a step of the first
+        constexpr int QR = TL::QR;                        // matrix instructions of each product
+        static_assert(QR == 2 * TL::DT, "as many of each");
         u32x4 va[2][TL::DT];
         u32x2 pk[2][2];
         // fp8 scales of four entries at a time, read a step or two before they are used
@@ -1198,47 +1203,67 @@ void attend_block_kernel(AttendArgs A) {
         };
         read_scales(0, sS[FP8 ? stage : 0][1] + 32 * sub);
         float sum = st.l;
-        // the products go before the other wave's softmax (bf16: mixed batch 607 -> 575 us); fp8 waves
-        // also widen codes, which must not wait (64-draft trees 1,154 us with, 962 us without)
-        if constexpr (!FP8) __builtin_amdgcn_s_setprio(1);
+        // the products go before the other wave's staging and maxima (without: prefill 303 / 296 us,
+        // ragged batch 466 / 455 us, 64-draft fp8 trees 894 / 883 us)
+        __builtin_amdgcn_s_setprio(1);
         f32x16 s;
 #pragma unroll
         for (int v = 0; v < 16; ++v) s[v] = 0.f;
+        auto read_values = [&](int x) {                   // k step x / DT, values 32 (x % DT) and on
+            const uint8_t *row = vt + vo[x % TL::DT] + 16 * (x / TL::DT) * TL::ROW;
+            const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)row));
+            const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lds_s16x4 *)(row + 8 * TL::ROW)));
+            va[x / TL::DT][x % TL::DT] = u32x4{a[0], a[1], c[0], c[1]};
+        };
+        auto raise = [&](int v) {                         // entries v, v + 1
+            if (v % 4 == 0 && v < 12) read_scales(v / 4 + 1, sS[FP8 ? stage : 0][1] + 32 * sub);
+            if (v == 14) read_scales(0, sS[FP8 ? stage2 : 0][0] + 32 * sub2);
+            float p0 = __builtin_amdgcn_exp2f(fmaf(now[0][v], A.c, -st.mc));
+            float p1 = __builtin_amdgcn_exp2f(fmaf(now[0][v + 1], A.c, -st.mc));
+            sum += p0;
+            sum += p1;
+            if constexpr (FP8) {
+                p0 *= four[v / 4 & 1][v % 4];
+                p1 *= four[v / 4 & 1][v % 4 + 1];
+            }
+            pk[v / 8][v % 8 / 4][v % 4 / 2] = pack_bf16(p0, p1);
+        };
+        auto weigh_one = [&](int x) {
+            const u32x4 b = {pk[x / TL::DT][0][0], pk[x / TL::DT][0][1], pk[x / TL::DT][1][0], pk[x / TL::DT][1][1]};
+            st.o[x % TL::DT] = mma_bf16(va[x / TL::DT][x % TL::DT], b, st.o[x % TL::DT]);
+        };
+        // half of the scores, with the first k step's exponentials
+        constexpr int DT = TL::DT;
 #pragma unroll
-        for (int i = 0; i < QR; ++i) {
+        for (int i = 0; i < DT; ++i) {
             s = mma_bf16(ka[i], q[i], s);
+            read_values(i);
 #pragma unroll
-            for (int x = i * PV / QR; x < (i + 1) * PV / QR; ++x) {
-                const uint8_t *row = vt + vo[x % TL::DT] + 16 * (x / TL::DT) * TL::ROW;
-                const u32x2 a = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)row));
-                const u32x2 c = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (lds_s16x4 *)(row + 8 * TL::ROW)));
-                va[x / TL::DT][x % TL::DT] = u32x4{a[0], a[1], c[0], c[1]};
-            }
+            for (int v = 8 / DT * i; v < 8 / DT * (i + 1); v += 2) raise(v);
+            here(sum);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        // the other half in turn with that step's values, and the second step's exponentials
 #pragma unroll
-            for (int v = EX * i; v < EX * (i + 1); v += 2) {
-                if (v % 4 == 0 && v < 12) read_scales(v / 4 + 1, sS[FP8 ? stage : 0][1] + 32 * sub);
-                if (v == 14) read_scales(0, sS[FP8 ? stage2 : 0][0] + 32 * sub2);
-                float p0 = __builtin_amdgcn_exp2f(fmaf(now[0][v], A.c, -st.mc));
-                float p1 = __builtin_amdgcn_exp2f(fmaf(now[0][v + 1], A.c, -st.mc));
-                sum += p0;
-                sum += p1;
-                if constexpr (FP8) {
-                    p0 *= four[v / 4 & 1][v % 4];
-                    p1 *= four[v / 4 & 1][v % 4 + 1];
-                }
-                pk[v / 8][v % 8 / 4][v % 4 / 2] = pack_bf16(p0, p1);
-            }
+        for (int i = 0; i < DT; ++i) {
+            weigh_one(i);
+            read_values(DT + i);
+            raise(8 + 8 / DT * i);
+            here(sum);
+            __builtin_amdgcn_sched_barrier(0);
+            s = mma_bf16(ka[DT + i], q[DT + i], s);
+            if constexpr (DT == 2) raise(10 + 4 * i);
             here(sum);
             __builtin_amdgcn_sched_barrier(0);
         }
         st.l = sum;
+        // the second step's values, with the scores' scales and maximum
         float mx = kNegInf;
-        constexpr int MX = 16 / PV;
+        constexpr int MX = 16 / DT;
 #pragma unroll
-        for (int x = 0; x < PV; ++x) {
-            const u32x4 b = {pk[x / TL::DT][0][0], pk[x / TL::DT][0][1], pk[x / TL::DT][1][0], pk[x / TL::DT][1][1]};
-            st.o[x % TL::DT] = mma_bf16(va[x / TL::DT][x % TL::DT], b, st.o[x % TL::DT]);
+        for (int x = 0; x < DT; ++x) {
+            weigh_one(DT + x);
 #pragma unroll
             for (int v = MX * x; v < MX * (x + 1); ++v) {
                 if (v % 4 == 0 && v < 12) read_scales(v / 4 + 1, sS[FP8 ? stage2 : 0][0] + 32 * sub2);
@@ -1248,7 +1273,7 @@ void attend_block_kernel(AttendArgs A) {
             here(mx);
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!FP8) __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_s_setprio(0);
         then[0] = s;
         return mx;
     };
