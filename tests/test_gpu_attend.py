@@ -354,13 +354,21 @@ def test_ragged_batches(kind, D, ns, lens, window):
     H, K = 64, 8
     c = U.Cache(150, lens, K, D, kind)
     q = queries(151, sum(ns), H, D, kind)
-    got = U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0)
-    U.check_attend("ragged", c, got, U.attend_oracle(c, q, ns, D ** -0.5, window, 0))
+
+    def check(tag, got, bits=None):
+        pools = c.pools
+        for k in (0, 5):                                             # the oracle is slow: two kv heads of eight
+            c.pools, c.n_kv = [p[:, k:k + 1] for p in pools], 1
+            part = slice(8 * k, 8 * k + 8)
+            U.check_attend(f"{tag}, kv head {k}", c, (got[0][:, part], got[1][:, part]),
+                           U.attend_oracle(c, q[:, part], ns, D ** -0.5, window, 0, bits=bits))
+        c.pools, c.n_kv = pools, K
+
+    check("ragged", U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0))
     if max(ns) <= 64:
         bits = [U.tree_bits(np.random.default_rng(b), n) for b, n in enumerate(ns)]
         mask = U.pack_bits([r for x in bits for r in x], 1).to(DEV)
-        got = U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0, mask=mask)
-        U.check_attend("ragged trees", c, got, U.attend_oracle(c, q, ns, D ** -0.5, window, 0, bits=bits))
+        check("ragged trees", U.run_attend(c, q, starts(ns), max(ns), D ** -0.5, window, 0, mask=mask), bits)
 
 
 @pytest.mark.parametrize("ns", [[1, 2], [70, 40]])
