@@ -912,8 +912,8 @@ __device__ __forceinline__ Place place_of(const AttendArgs &A, int *ranked) {   
 // Workgroup (split, block of 128 columns, kv head, request) of four waves, 32 columns each; the
 // 32-entry tiles are shared.  The next tile's copy (two LDS stages) is in flight while a tile is
 // worked on, one barrier a tile.  Bound by the float32 MFMAs (154 TFLOP/s in a large product) and,
-// with one workgroup a CU, by the latency from scores to sums: 5.3 to 5.8 us a tile of 128 x 128
-// either way.  3 requests of up to 333 rows x 12 heads of 64 dims: 26 us and 4 us to join.
+// with one workgroup a CU, by the latency from scores to sums: 5.3 to 5.8 us a tile of 32 entries
+// of 128 dims either way.  3 requests of up to 333 rows x 12 heads of 64 dims: 25 us and 5 us to join.
 template <int D>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2)))
 void attend_tile_kernel(AttendArgs A) {
@@ -1001,12 +1001,12 @@ void attend_tile_kernel(AttendArgs A) {
 // prefill 287 / 296 us, ragged batch 460 / 481 us; the swizzle is then the source address's, a lane.)
 //
 // Bound by instruction issue and by the clock under this load (1.9 GHz; the same prefill over zeros
-// takes 258 us instead of 296): the MFMAs are busy 41% of the cycles and the vector units 43%, a
-// third of the former beside the latter; the rest is the maximum's lane swap and branch, the
-// barrier (without it, in a timing copy, 262 of 315 us) and waits for LDS.  4,096 rows x 32 heads
+// takes 258 us instead of 296): the MFMAs are busy 44% of the cycles and the vector units 47%, half
+// of the former beside the latter; the rest is the maximum's lane swap and branch, the barrier
+// (without it, in a timing copy, 262 of 315 us) and waits for LDS.  4,096 rows x 32 heads
 // under a window: 290 us, 949 TFLOP/s (a large bf16 product: 1,236).  8 ragged requests over 8,192
 // entries 455 us, 910 TFLOP/s.  fp8 also widens codes and multiplies two scales: 30 trees of 64
-// drafts over up to 24,576 entries 880 us, 760 TFLOP/s, on 240 of 256 CUs.
+// drafts over up to 24,576 entries 870 us, 770 TFLOP/s, on 240 of 256 CUs.
 constexpr int kBlockNT = 512;
 template <int FMT, int D>
 struct Staged {

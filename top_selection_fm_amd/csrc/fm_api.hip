@@ -639,10 +639,10 @@ fm_status check_attend(const fm_attn_desc *a, const fm_kv_desc *kv, int64_t wind
 // The entries of a block are split over S workgroups where that ends sooner by this estimate (us;
 // measured per kernel with head_dim 128): rounds of workgroups over the chip x (tiles a workgroup x
 // time a tile + a workgroup's start and end), and for S > 1 the joining launch and its traffic.
-// Measured: 16 drafts x 4 heads over 2,000 entries 48 us whole, 21 us in 4 parts, 14 us in 16; 8
-// ragged requests over 8,192 entries 454 us whole, 544 us in 2; 30 x 32,768 fp8 entries 389 us
-// whole, 398 us in 2, 419 us in 6; 30 trees of 64 drafts over up to 24,576 entries 951 us whole,
-// 922 us in 2 (by the estimate the same; their lengths, which it does not know, differ by a third).
+// Measured: 16 drafts x 4 heads over 2,000 entries 47 us whole, 21 us in 4 parts, 14 us in 16; 8
+// ragged requests over 8,192 entries 448 us whole, 529 us in 2; 30 x 32,768 fp8 entries 389 us
+// whole, 398 us in 2, 419 us in 6; 30 trees of 64 drafts over up to 24,576 fp8 entries 847 us
+// whole, 902 us in 2.
 struct AttendPlan {
     int columns, blocks, splits, ranked;
     size_t ml_bytes, o_bytes;
