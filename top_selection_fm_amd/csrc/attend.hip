@@ -216,7 +216,9 @@ template <int FMT, int D>
 struct State {
     f32x16 o[Tile<FMT, D>::DT];
     float m, l;       // m: maximum in score units (both halves alike), l: the lane's own entries
-    float mc;         // m times c, 0 while nothing was seen
+    // what exponentials are taken against: m times c, or for float32 m (a difference first, so that an
+    // exponent's error goes with its size and not the maximum's); 0 while nothing was seen
+    float mc;
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int t = 0; t < Tile<FMT, D>::DT; ++t)
@@ -499,7 +501,7 @@ __device__ __forceinline__ void raise_max(float mx, float c, State<FMT, D> &st) 
         const float m = fmaxf(st.m, mx);
         const float a = st.m == kNegInf ? 0.f : __builtin_amdgcn_exp2f((st.m - m) * c);
         st.m = m;
-        st.mc = m == kNegInf ? 0.f : m * c;
+        st.mc = m == kNegInf ? 0.f : FMT == KEY_F32 ? m : m * c;
         st.l *= a;
 #pragma unroll
         for (int t = 0; t < Tile<FMT, D>::DT; ++t)
@@ -518,7 +520,7 @@ __device__ __forceinline__ void exponentials(SRegs<NS> &s, bool masked, float c,
     for (int sub = 0; sub < NS; ++sub)
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            s[sub][v] = __builtin_amdgcn_exp2f(fmaf(s[sub][v], c, -st.mc));
+            s[sub][v] = __builtin_amdgcn_exp2f(FMT == KEY_F32 ? (s[sub][v] - st.mc) * c : fmaf(s[sub][v], c, -st.mc));
             sum[v & 1] += s[sub][v];
         }
     st.l = sum[0] + sum[1];
